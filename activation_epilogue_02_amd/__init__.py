@@ -17,3 +17,4 @@ from .binding import (GE_BIAS_COL, GE_BIAS_ROW, GE_EPILOG_BIAS, GE_EPILOG_DGELU,
                       gemm_epilog_free, gemm_epilog_plan,
                       gemm_epilog_status_string, gemm_epilog_workspace_size, ge_desc, ge_pref,
                       make_desc)
+from .norm import GE_NORM_E4M3_ROW, GE_NORM_MX, GE_NORM_PLAIN, RmsNorm  # noqa: F401

@@ -67,6 +67,12 @@ class ge_batch_strides(ctypes.Structure):
                 ("d", ctypes.c_int64), ("aux", ctypes.c_int64)]
 
 
+class ge_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("out", ctypes.c_int32), ("ld", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
+
+
 class GemmEpilogError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -102,6 +108,13 @@ def lib():
         L.gemm_epilog_execute_m.argtypes = [vp, ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.gemm_epilog_set_batch_strides.argtypes = [vp, ctypes.POINTER(ge_batch_strides)]
         L.gemm_epilog_set_fp8_output.argtypes = [vp, vp, vp]
+        i64 = ctypes.c_int64
+        L.ge_rms_norm_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(ge_norm_desc)]
+        L.ge_rms_norm_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+        L.ge_rms_norm_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.ge_rms_norm_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.ge_rms_norm_describe.argtypes = [vp, ctypes.c_char_p, sz]
+        L.ge_rms_norm_free.argtypes = [vp]
         for f in ("gemm_epilog_create", "gemm_epilog_plan", "gemm_epilog_workspace_size",
                   "gemm_epilog_aux_ld", "gemm_epilog_execute", "gemm_epilog_free",
                   "gemm_epilog_describe", "gemm_epilog_autotune", "gemm_epilog_execute_c",
@@ -122,6 +135,13 @@ def _ptr(x) -> Optional[int]:
     if isinstance(x, torch.Tensor):
         return x.data_ptr()
     return int(x)
+
+
+def _stream(stream) -> Optional[int]:
+    """The handle of a torch stream (default: the current one), or a raw one."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def make_desc(m, n, k, a_type, d_type, op_b=GE_OP_N, lda=None, ldb=None, ldd=None,

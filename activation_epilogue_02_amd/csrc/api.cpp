@@ -14,6 +14,7 @@
 #include <mutex>
 #include <new>
 
+#include "ge_host.h"
 #include "ge_params.h"
 
 using namespace ge;
@@ -73,17 +74,6 @@ struct ge_plan_s {
 
 namespace {
 
-int elem_size(int t) {
-    switch (t) {
-    case GE_F32: return 4;
-    case GE_F16: return 2;
-    case GE_BF16: return 2;
-    case GE_F8_E4M3: return 1;
-    case GE_MXF8_E4M3: return 1;
-    }
-    return 0;
-}
-
 bool dtype_combo_ok(int a, int b, int d) {
     if (a != b) return false;
     switch (a) {
@@ -95,8 +85,6 @@ bool dtype_combo_ok(int a, int b, int d) {
     }
     return false;
 }
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Epilogues that add a bias (DRELU and DGELU read none).
 bool has_bias(int e) {
@@ -115,15 +103,11 @@ bool aux_is_matrix(int e) {
     return e == GE_EPILOG_GELU_AUX_BIAS || e == GE_EPILOG_DGELU || e == GE_EPILOG_DGELU_BGRAD;
 }
 
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 const TileShape* find_tile(int id) {
     for (int i = 0; i < kNumTiles; ++i)
         if (kTiles[i].id == id) return &kTiles[i];
     return nullptr;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The register-staged tile kernel's tile for a problem (any dtype).
 int choose_tile_plain(int64_t m, int64_t n) {
@@ -257,18 +241,6 @@ int smallm_auto_split(int64_t tiles_n, int64_t spans) {
     int split = 1;
     while (tiles_n * split * 2 <= kCUs && spans >= split * 2 * kWaves * kMinSpansPerWave) split *= 2;
     return split;
-}
-
-// GE_LOG=1 in the environment: every successful plan prints its
-// description (path, tile, grid, split, workspace) to stderr.
-bool plan_log() {
-    const char* e = getenv("GE_LOG");
-    return e && e[0] == '1';
-}
-
-bool test_fail_launch() {
-    const char* e = getenv("GE_TEST_FAIL_LAUNCH");
-    return e && e[0] == '1';
 }
 
 }  // namespace

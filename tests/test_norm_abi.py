@@ -1,0 +1,154 @@
+"""The RMS norm's C ABI without a GPU: descriptions and calls that it refuses
+before any HIP call, launch shapes, workspace sizes and the rules for optional
+buffers.  Addresses here are numbers that are never read."""
+import ctypes
+
+import pytest
+
+from activation_epilogue_02_amd import RmsNorm
+from activation_epilogue_02_amd import binding as B
+
+P = 0x10000   # a 16-byte aligned address
+
+
+def create(rows=4, cols=64, type_=B.GE_BF16, out=0, ld=64, ldy=64, eps=1e-6):
+    h = ctypes.c_void_p()
+    d = B.ge_norm_desc(rows, cols, type_, out, ld, ldy, eps)
+    return B.lib().ge_rms_norm_create(ctypes.byref(h), ctypes.byref(d)), h.value
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), B.GE_OK),
+    (dict(rows=0), B.GE_OK),
+    (dict(rows=-1), B.GE_ERR_SHAPE),
+    (dict(rows=1 << 31), B.GE_ERR_SHAPE),
+    (dict(cols=0), B.GE_ERR_SHAPE),
+    (dict(cols=65), B.GE_ERR_SHAPE),              # ld and ldy below cols
+    (dict(cols=65, ld=72, ldy=64), B.GE_ERR_SHAPE),
+    (dict(cols=65, ld=72, ldy=72), B.GE_OK),
+    (dict(ld=68), B.GE_ERR_ALIGN),
+    (dict(ldy=68), B.GE_ERR_ALIGN),
+    (dict(type_=B.GE_F32, ld=68, ldy=68), B.GE_OK),
+    (dict(out=1, ldy=72), B.GE_ERR_ALIGN),        # 8-bit rows: 16 bytes are 16 values
+    (dict(out=2, ldy=80), B.GE_OK),
+    (dict(out=3), B.GE_ERR_SHAPE),
+    (dict(out=-1), B.GE_ERR_SHAPE),
+    (dict(type_=B.GE_F8_E4M3), B.GE_ERR_DTYPE),
+    (dict(type_=9), B.GE_ERR_DTYPE),
+    (dict(eps=0.0), B.GE_OK),
+    (dict(eps=-1e-6), B.GE_ERR_SHAPE),
+    (dict(eps=float("nan")), B.GE_ERR_SHAPE),
+    (dict(eps=float("inf")), B.GE_ERR_SHAPE),
+], ids=str)
+def test_create(kw, status):
+    st, h = create(**kw)
+    assert st == status
+    assert (h is not None) == (status == B.GE_OK)
+    assert B.lib().ge_rms_norm_free(h) == B.GE_OK
+
+
+def test_null_arguments():
+    L = B.lib()
+    h = ctypes.c_void_p()
+    d = B.ge_norm_desc(4, 64, B.GE_BF16, 0, 64, 64, 1e-6)
+    assert L.ge_rms_norm_create(None, ctypes.byref(d)) == B.GE_ERR_NULL
+    assert L.ge_rms_norm_create(ctypes.byref(h), None) == B.GE_ERR_NULL
+    assert L.ge_rms_norm_workspace_size(None, ctypes.byref(ctypes.c_size_t())) == B.GE_ERR_NULL
+    assert L.ge_rms_norm_describe(None, None, 0) == B.GE_ERR_NULL
+    assert L.ge_rms_norm_forward(None, 0, *[None] * 8) == B.GE_ERR_NULL
+    assert L.ge_rms_norm_backward(None, 0, *[None] * 8, 0, None) == B.GE_ERR_NULL
+    assert L.ge_rms_norm_free(None) == B.GE_OK
+
+
+def forward(h, rows=4, x=P, res=None, gamma=P, hs=None, y=P, scales=None, rstd=None):
+    return B.lib().ge_rms_norm_forward(h, rows, x, res, gamma, hs, y, scales, rstd, None)
+
+
+@pytest.mark.parametrize("out,kw,status", [
+    (0, dict(x=None), B.GE_ERR_NULL),
+    (0, dict(gamma=None), B.GE_ERR_NULL),
+    (0, dict(y=None), B.GE_ERR_NULL),
+    (0, dict(rows=5), B.GE_ERR_SHAPE),
+    (0, dict(rows=-1), B.GE_ERR_SHAPE),
+    (0, dict(hs=P), B.GE_ERR_EPILOG),             # h without a residual is x itself
+    (0, dict(scales=P), B.GE_ERR_EPILOG),
+    (1, dict(), B.GE_ERR_EPILOG),                 # the scales are missing
+    (2, dict(), B.GE_ERR_EPILOG),
+    (0, dict(x=P + 8), B.GE_ERR_ALIGN),
+    (0, dict(res=P + 2), B.GE_ERR_ALIGN),
+    (0, dict(gamma=P + 4), B.GE_ERR_ALIGN),
+    (0, dict(res=P, hs=P + 8), B.GE_ERR_ALIGN),
+    (0, dict(y=P + 8), B.GE_ERR_ALIGN),
+    (0, dict(rstd=P + 2), B.GE_ERR_ALIGN),
+    (1, dict(scales=P + 2), B.GE_ERR_ALIGN),
+    (2, dict(scales=P + 4), B.GE_ERR_ALIGN),
+    (0, dict(rows=0, x=None, y=None), B.GE_OK),
+    (1, dict(rows=0, x=None, y=None), B.GE_OK),
+], ids=str)
+def test_forward_refusals(out, kw, status):
+    st, h = create(out=out)
+    assert st == B.GE_OK
+    assert forward(h, **kw) == status
+    B.lib().ge_rms_norm_free(h)
+
+
+def backward(h, rows=4, dy=P, hs=P, gamma=P, rstd=P, dh=None, dx=P, dgamma=None, ws=None, n=0):
+    return B.lib().ge_rms_norm_backward(h, rows, dy, hs, gamma, rstd, dh, dx, dgamma, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), B.GE_ERR_NULL),
+    (dict(hs=None), B.GE_ERR_NULL),
+    (dict(gamma=None), B.GE_ERR_NULL),
+    (dict(rstd=None), B.GE_ERR_NULL),
+    (dict(dx=None), B.GE_ERR_NULL),
+    (dict(rows=5), B.GE_ERR_SHAPE),
+    (dict(dgamma=P), B.GE_ERR_WORKSPACE),
+    (dict(dgamma=P, ws=P, n=255), B.GE_ERR_WORKSPACE),
+    (dict(dh=P + 8), B.GE_ERR_ALIGN),
+    (dict(dx=P + 8), B.GE_ERR_ALIGN),
+    (dict(dy=P + 8), B.GE_ERR_ALIGN),
+    (dict(dgamma=P + 8, ws=P, n=1 << 20), B.GE_ERR_ALIGN),
+    (dict(dgamma=P, ws=P + 8, n=1 << 20), B.GE_ERR_ALIGN),
+    (dict(rows=0, dy=None, hs=None, rstd=None, dx=None), B.GE_OK),
+], ids=str)
+def test_backward_refusals(kw, status):
+    st, h = create()
+    assert st == B.GE_OK
+    assert backward(h, **kw) == status
+    B.lib().ge_rms_norm_free(h)
+
+
+def test_launch_failure_is_reported(monkeypatch):
+    monkeypatch.setenv("GE_TEST_FAIL_LAUNCH", "1")
+    _, h = create()
+    assert forward(h) == B.GE_ERR_HIP
+    assert backward(h) == B.GE_ERR_HIP
+    B.lib().ge_rms_norm_free(h)
+
+
+@pytest.mark.parametrize("dtype,per", [("bf16", 8), ("f16", 8), ("f32", 4)])
+def test_every_row_length_has_a_shape(dtype, per):
+    """The shape holds the row (threads * chunks * values per chunk), or is
+    the one for rows of any length."""
+    for cols in (1, per, 64 * per, 64 * per + 1, 128 * per, 1023, 256 * per, 256 * per + 1, 1024 * per, 1024 * per + 1,
+                 4096 * per, 4096 * per + 1, 1 << 20):
+        with RmsNorm(8, cols, dtype) as n:
+            d = dict(kv.split("=") for kv in n.describe().split())
+            for which in ("forward", "backward"):
+                t, c = map(int, d[which].split("x"))
+                assert t * c * per >= cols or (c == 0 and cols > 4096 * per), (cols, which, d)
+            assert n.workspace_bytes >= int(d["blocks"]) * cols * 4
+            assert 1 <= int(d["blocks"]) <= 1024
+
+
+def test_wrapper_refuses_other_types_and_strides():
+    import torch
+    with RmsNorm(4, 64, "bf16", ld=64) as n:
+        ok = torch.zeros(4, 64, dtype=torch.bfloat16)
+        with pytest.raises(B.GemmEpilogError) as e:
+            n.forward(ok.float(), ok[0], ok)
+        assert e.value.status == B.GE_ERR_DTYPE
+        with pytest.raises(B.GemmEpilogError) as e:
+            n.forward(torch.zeros(4, 72, dtype=torch.bfloat16)[:, :64], ok[0], ok)
+        assert e.value.status == B.GE_ERR_SHAPE
