@@ -304,8 +304,10 @@ ge_tile_kernel(KernelArgs p_all) {
 
     // ---- main loop: double-buffered LDS, one barrier per K step ----
     const int KT = (K + BK - 1) / BK;
-    load_regs(0);
-    store_lds(0);
+    if (KT > 0) {   // k = 0 reads nothing: A and B may be NULL
+        load_regs(0);
+        store_lds(0);
+    }
     __syncthreads();
     for (int kt = 0; kt < KT; ++kt) {
         const int cur = kt & 1;
