@@ -109,6 +109,12 @@ def lib():
         L.gemm_epilog_set_batch_strides.argtypes = [vp, ctypes.POINTER(ge_batch_strides)]
         L.gemm_epilog_set_fp8_output.argtypes = [vp, vp, vp]
         i64 = ctypes.c_int64
+        L.gemm_epilog_plan_residual.argtypes = [vp, i32, i32]
+        L.gemm_epilog_execute_residual.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp,
+                                                   sz, vp]
+        L.gemm_epilog_plan_backward.argtypes = [vp]
+        L.gemm_epilog_backward_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+        L.gemm_epilog_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.ge_rms_norm_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(ge_norm_desc)]
         L.ge_rms_norm_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
         L.ge_rms_norm_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -291,6 +297,43 @@ def gemm_epilog_autotune(h: int, A, B, bias, D, aux=None, scale_a=None, scale_b=
     return best.value
 
 
+def gemm_epilog_plan_residual(h: int, epilog, axis=GE_BIAS_COL) -> None:
+    e = EPILOG_CODE[epilog] if isinstance(epilog, str) else epilog
+    a = AXIS_CODE[axis] if isinstance(axis, str) else axis
+    _check(lib().gemm_epilog_plan_residual(h, e, a), "gemm_epilog_plan_residual")
+
+
+def gemm_epilog_execute_residual(h: int, m: int, A, B, bias, residual, ldr: int, D, aux=None, row_scale=None,
+                                 col_scale=None, a_scales=None, b_scales=None, scale_a=None, scale_b=None,
+                                 workspace=None, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """D = residual + act(s * row_scale[i] * col_scale[j] * A*B + bias) for m rows."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().gemm_epilog_execute_residual(
+        h, m, _ptr(A), _ptr(B), _ptr(a_scales), _ptr(b_scales), _ptr(bias), _ptr(residual), ldr, _ptr(row_scale),
+        _ptr(col_scale), _ptr(scale_a), _ptr(scale_b), _ptr(D), _ptr(aux), _ptr(workspace), workspace_bytes,
+        _stream(stream)), "gemm_epilog_execute_residual")
+
+
+def gemm_epilog_plan_backward(h: int) -> None:
+    _check(lib().gemm_epilog_plan_backward(h), "gemm_epilog_plan_backward")
+
+
+def gemm_epilog_backward_workspace_size(h: int) -> int:
+    s = ctypes.c_size_t()
+    _check(lib().gemm_epilog_backward_workspace_size(h, ctypes.byref(s)), "gemm_epilog_backward_workspace_size")
+    return s.value
+
+
+def gemm_epilog_backward(h: int, dD, A, B, aux, dA, dB, dbias=None, workspace=None,
+                         workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """Gradients of the residual product's inputs (any of dA, dB, dbias may be None)."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().gemm_epilog_backward(h, _ptr(dD), _ptr(A), _ptr(B), _ptr(aux), _ptr(dA), _ptr(dB), _ptr(dbias),
+                                      _ptr(workspace), workspace_bytes, _stream(stream)), "gemm_epilog_backward")
+
+
 def gemm_epilog_describe(h: int) -> str:
     buf = ctypes.create_string_buffer(512)
     _check(lib().gemm_epilog_describe(h, buf, 512), "gemm_epilog_describe")
@@ -345,6 +388,47 @@ class GemmEpilog:
                             None if workspace is None else workspace.numel() * workspace.element_size(),
                             stream)
         return D, aux
+
+    def plan_residual(self, epilog="bias", axis="col"):
+        """Plan for execute_residual: D = residual + act(P), P = s * row_scale[i] * col_scale[j] * A*B + bias."""
+        gemm_epilog_plan_residual(self.h, epilog, axis)
+        self.epilog = EPILOG_CODE[epilog] if isinstance(epilog, str) else epilog
+        self.ws_bytes = gemm_epilog_workspace_size(self.h)
+        self.aux_ld_bits = gemm_epilog_aux_ld(self.h)
+        return self
+
+    def execute_residual(self, A, B, bias=None, residual=None, D=None, aux=None, row_scale=None, col_scale=None,
+                         a_scales=None, b_scales=None, scale_a=None, scale_b=None, workspace=None, m=None,
+                         stream=None):
+        """residual is an m x n matrix in D's dtype (any 16-byte row stride), or None; m: rows of this call."""
+        if D is None:
+            D, aux_new, ws_new = self.alloc_outputs(A.device)
+            aux = aux if aux is not None else aux_new
+            workspace = workspace if workspace is not None else ws_new
+        d = self.desc
+        rows = d.m if m is None else m
+        ldr = d.ldd
+        if residual is not None and residual.dtype != D.dtype:
+            raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: residual")
+        if rows > 1:   # (a single row has no stride of its own)
+            if A.stride(0) != d.lda or D.stride(0) != d.ldd:
+                raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: A or D")
+            if residual is not None:
+                ldr = residual.stride(0)
+        gemm_epilog_execute_residual(self.h, rows, A, B, bias, residual, ldr, D, aux, row_scale, col_scale, a_scales,
+                                     b_scales, scale_a, scale_b, workspace, None, stream)
+        return D, aux
+
+    def plan_backward(self):
+        """Plan the backward pass of the residual product (after plan_residual)."""
+        gemm_epilog_plan_backward(self.h)
+        self.backward_ws_bytes = gemm_epilog_backward_workspace_size(self.h)
+        return self
+
+    def backward(self, dD, A, B, dA=None, dB=None, dbias=None, aux=None, workspace=None, stream=None):
+        """Writes dA, dB and dbias (those given); dD has D's layout, dA A's and dB B's."""
+        gemm_epilog_backward(self.h, dD, A, B, aux, dA, dB, dbias, workspace, None, stream)
+        return dA, dB, dbias
 
     def describe(self) -> str:
         return gemm_epilog_describe(self.h)

@@ -15,6 +15,7 @@
 #include <new>
 
 #include "ge_host.h"
+#include "grad_params.h"
 #include "ge_params.h"
 
 using namespace ge;
@@ -70,6 +71,18 @@ struct ge_plan_s {
     ge_batch_strides bstr = {0, 0, 0, 0, 0};
     const float* scale_d = nullptr;   // fp8 output: D's scale (NULL = 1)
     float* amax_d = nullptr;          // fp8 output: largest |y| per product, or NULL
+    // residual product (gemm_epilog_plan_residual): the plan is for
+    // execute_residual only; skinny_mb = row groups of the streaming kernel
+    bool residual = false;
+    int32_t skinny_mb = 0;
+    // its backward pass (gemm_epilog_plan_backward): dP (bytes, row stride),
+    // the transposed operand of the weight's gradient, the bias partials, and
+    // the two products' handles (owned by the handle)
+    bool backward = false;
+    size_t bw_dp = 0, bw_t = 0, bw_part = 0, bw_gemm = 0;
+    int64_t ld_dp = 0, ld_t = 0;
+    ge_plan_s* g_a = nullptr;
+    ge_plan_s* g_b = nullptr;
 };
 
 namespace {
@@ -107,6 +120,40 @@ const TileShape* find_tile(int id) {
     for (int i = 0; i < kNumTiles; ++i)
         if (kTiles[i].id == id) return &kTiles[i];
     return nullptr;
+}
+
+const TileShape* find_res_tile(int id) {
+    for (int i = 0; i < kNumResTiles; ++i)
+        if (kResTiles[i].id == id) return &kResTiles[i];
+    return nullptr;
+}
+
+// The residual product's tile: the largest that gives the CUs work, and below
+// that the smallest, which splits K.
+int choose_res_tile(const ge_desc& d) {
+    const int64_t t256 = ceil_div(d.m, 256) * ceil_div(d.n, 256);
+    const int64_t t128 = ceil_div(d.m, 128) * ceil_div(d.n, 128);
+    switch (d.a_type) {
+    case GE_F32: return t128 >= 256 ? 2 : 1;
+    case GE_MXF8_E4M3: return 18;
+    case GE_F8_E4M3:
+        if (t256 >= 512) return 16;
+        if (ceil_div(d.m, 256) * ceil_div(d.n, 128) >= 512) return 15;
+        return t128 >= 256 ? 8 : 17;
+    }
+    if (t256 >= 512) return 6;
+    return t128 >= 256 ? 8 : 14;
+}
+
+// K slices of a split-K tile: the largest power of two that keeps the grid
+// within one workgroup per CU and every slice at 16 or more steps (32 beyond
+// 128 workgroups), at most 8 (16 for at most 4 tiles).
+int res_split(int64_t tiles, int64_t steps) {
+    const int cap = tiles <= 4 ? 16 : 8;
+    int split = 1;
+    while (split * 2 <= cap && tiles * split * 2 <= 256 && steps >= split * 2 * (tiles * split * 2 > 128 ? 32 : 16))
+        split *= 2;
+    return split;
 }
 
 // The register-staged tile kernel's tile for a problem (any dtype).
@@ -283,6 +330,7 @@ int gemm_epilog_plan(ge_handle h, int32_t epilog, int32_t bias_axis, const ge_pr
 
     ge_plan_s q = *h;
     q.planned = false;
+    q.residual = q.backward = false;
     q.k_stagger = 0;
     q.epilog = epilog;
     q.axis = bias_axis;
@@ -499,7 +547,7 @@ static int execute_impl(ge_handle h, const void* A, const void* B, const void* c
                         void* workspace, size_t workspace_bytes, void* stream, bool static_ws = false,
                         const void* mx_a = nullptr, const void* mx_b = nullptr, int64_t m_run = -1) {
     if (!h) return GE_ERR_NULL;
-    if (!h->planned) return GE_ERR_STATE;
+    if (!h->planned || h->residual) return GE_ERR_STATE;
     const ge_desc& d = h->d;
     if (m_run > d.m) return GE_ERR_SHAPE;
     const int64_t M = m_run >= 0 ? m_run : d.m;   // rows of this call
@@ -715,7 +763,291 @@ int gemm_epilog_execute_static(ge_handle h, const void* A, const void* B, const 
     return execute_impl(h, A, B, nullptr, 0, nullptr, bias, D, aux, scale_a, scale_b, nullptr, 0, stream, true);
 }
 
+// ---- residual product ---------------------------------------------------------
+int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis) {
+    if (!h) return GE_ERR_NULL;
+    const bool known = epilog == GE_EPILOG_NONE || has_bias(epilog);
+    if (!known || (bias_axis != GE_BIAS_ROW && bias_axis != GE_BIAS_COL)) return GE_ERR_EPILOG;
+    const ge_desc& d = h->d;
+    if (d.batch > 1) return GE_ERR_SHAPE;
+    if (d.d_type == GE_F8_E4M3) return GE_ERR_DTYPE;
+    ge_plan_s q = *h;
+    q.planned = true;
+    q.residual = true;
+    q.backward = false;
+    q.epilog = epilog;
+    q.axis = bias_axis;
+    q.unfused = 0;
+    q.pref = {0, 0, 0, 0, 0};
+    q.k_stagger = 0;
+    q.split_k = 1;
+    q.k_per_split = (int32_t)d.k;
+    q.ws_c = q.ws_partial = q.ws_counters = q.ws_bgrad = 0;
+    q.n_counters = q.part_bytes = 0;
+    q.bgrad_parts = 0;
+    q.ldaux = !has_aux(epilog) ? 0
+              : aux_is_matrix(epilog) ? (int64_t)round_up((size_t)d.n, 128)
+                                      : (int64_t)round_up((size_t)d.n, 128) / 32;
+    if (q.ldaux > INT32_MAX) return GE_ERR_SHAPE;
+    if (d.m <= 64 && d.op_b == GE_OP_T && d.a_type != GE_F32) {
+        // few rows and a weight given n x k: W is streamed once
+        q.path = PATH_SKINNY;
+        q.tile_id = 0;
+        q.skinny_mb = d.m <= 16 ? 1 : d.m <= 32 ? 2 : 4;
+        q.group_m = ceil_div(d.n, 32) >= 256 ? 2 : 1;
+        q.tiles_m = 1;
+        q.tiles_n = (int32_t)ceil_div(d.n, 16 * q.group_m);
+        q.grid = (unsigned)q.tiles_n;
+    } else {
+        q.path = PATH_TILE;
+        q.tile_id = choose_res_tile(d);
+        const TileShape* t = find_res_tile(q.tile_id);
+        if (!tile_span_ok(t, d)) return GE_ERR_SHAPE;
+        const int64_t tm = ceil_div(d.m, t->bm), tn = ceil_div(d.n, t->bn);
+        if (tm * tn > INT32_MAX) return GE_ERR_SHAPE;
+        q.tiles_m = (int32_t)tm;
+        q.tiles_n = (int32_t)tn;
+        q.group_m = auto_group_m(t, tm, d.a_type);
+        q.k_stagger = auto_k_stagger(t, d.a_type);
+        q.grid = (unsigned)(tm * tn);
+        if (t->kernel == 5) {
+            const int64_t step = elem_size(d.a_type) == 2 ? 64 : 128, steps = ceil_div(d.k, step);
+            int split = res_split(tm * tn, steps);
+            if (split > steps) split = steps > 0 ? (int)steps : 1;
+            q.k_per_split = (int32_t)(ceil_div(steps, split) * step);
+            q.split_k = q.k_per_split > 0 ? (int32_t)ceil_div(d.k, q.k_per_split) : 1;
+            if (q.split_k < 1) q.split_k = 1;
+            if (q.split_k > 1) {
+                q.n_counters = tm * tn;
+                q.part_bytes = tm * tn * q.split_k * (int64_t)t->bm * t->bn * (int64_t)sizeof(float);
+                q.ws_partial = round_up((size_t)q.part_bytes, 256);
+                q.ws_counters = round_up((size_t)q.n_counters * sizeof(uint32_t), 256);
+            }
+        }
+    }
+    *h = q;
+    if (plan_log()) {
+        char line[512];
+        gemm_epilog_describe(h, line, sizeof line);
+        fprintf(stderr, "gemm_epilog: residual plan %s\n", line);
+    }
+    return GE_OK;
+}
+
+int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const void* B, const void* a_scales,
+                                 const void* b_scales, const void* bias, const void* residual, int64_t ldr,
+                                 const float* row_scale, const float* col_scale, const float* scale_a,
+                                 const float* scale_b, void* D, void* aux, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    if (!h) return GE_ERR_NULL;
+    if (!h->planned || !h->residual) return GE_ERR_STATE;
+    const ge_desc& d = h->d;
+    if (m < 0 || m > d.m) return GE_ERR_SHAPE;
+    const bool mx = d.a_type == GE_MXF8_E4M3;
+    if (!mx && (a_scales || b_scales)) return GE_ERR_DTYPE;
+    if (mx && ((!a_scales && m * d.k > 0) || (!b_scales && d.n * d.k > 0))) return GE_ERR_NULL;
+    if ((!A && m * d.k > 0) || (!B && d.k * d.n > 0) || (!D && m * d.n > 0)) return GE_ERR_NULL;
+    if (has_bias(h->epilog) && !bias && (h->axis == GE_BIAS_ROW ? m : d.n) > 0) return GE_ERR_NULL;
+    if (aux && !has_aux(h->epilog)) return GE_ERR_EPILOG;
+    if (!aux && has_aux(h->epilog) && m * d.n > 0) return GE_ERR_EPILOG;
+    if (residual && ldr < d.n) return GE_ERR_SHAPE;
+    if (residual && (ldr * elem_size(d.d_type)) % 16) return GE_ERR_ALIGN;
+    if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || !aligned(bias, 16) || !aligned(aux, 16) ||
+        !aligned(a_scales, 16) || !aligned(b_scales, 16) || !aligned(residual, 16) || !aligned(col_scale, 16) ||
+        !aligned(workspace, 16) || !aligned(row_scale, 4) || !aligned(scale_a, 4) || !aligned(scale_b, 4))
+        return GE_ERR_ALIGN;
+    const size_t need = h->ws_partial + h->ws_counters;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GE_ERR_WORKSPACE;
+    if (test_fail_launch()) return GE_ERR_HIP;
+    if (m == 0 || d.n == 0) return GE_OK;
+
+    KernelArgs a;
+    memset(&a, 0, sizeof(a));
+    a.A = A;
+    a.B = B;
+    a.bias = has_bias(h->epilog) ? bias : nullptr;
+    a.D = D;
+    a.aux = (uint32_t*)aux;
+    a.scale_a = scale_a;
+    a.scale_b = scale_b;
+    a.m = (int32_t)m;
+    a.n = (int32_t)d.n;
+    a.k = (int32_t)d.k;
+    a.epilog = h->epilog;
+    a.axis = h->axis;
+    a.ldaux = (int32_t)h->ldaux;
+    a.lda = d.lda;
+    a.ldb = d.ldb;
+    a.ldd = d.ldd;
+    a.tiles_m = h->tiles_m;
+    a.tiles_n = h->tiles_n;
+    a.group_m = h->group_m;
+    a.split_k = h->split_k;
+    a.k_per_split = h->k_per_split;
+    a.k_stagger = h->k_stagger;
+    a.batch = 1;
+    ResArgs r = {};
+    r.sa = (const uint8_t*)a_scales;
+    r.sb = (const uint8_t*)b_scales;
+    r.ld = (int32_t)GE_MX_SCALE_LD(d.k);
+    r.kb = (int32_t)ceil_div(d.k, 32);
+    r.res = residual;
+    r.row_scale = row_scale;
+    r.col_scale = col_scale;
+    r.ldr = ldr;
+    if (h->path == PATH_SKINNY)
+        return launch_skinny(d.a_type, d.d_type, h->skinny_mb, h->group_m, a, r, h->grid, stream) == 0 ? GE_OK
+                                                                                                      : GE_ERR_HIP;
+    unsigned grid = h->grid;
+    if (m != d.m) {
+        a.tiles_m = (int32_t)ceil_div(m, find_res_tile(h->tile_id)->bm);
+        grid = (unsigned)(a.tiles_m * (int64_t)a.tiles_n);
+    }
+    if (h->split_k > 1) {
+        a.partial = (float*)workspace;
+        a.counters = (uint32_t*)((uint8_t*)workspace + h->ws_partial);
+        if (launch_clear_counters(a.counters, (int)h->n_counters, stream) != 0) return GE_ERR_HIP;
+    }
+    return launch_tile_res(h->tile_id, d.a_type, d.d_type, d.op_b, a, r, grid, stream) == 0 ? GE_OK : GE_ERR_HIP;
+}
+
+// ---- its backward pass ----------------------------------------------------------
+// dA (m x k) = dP B^T and dB = A^T dP (k x n) or dP^T A (n x k), both on the
+// tile kernels.  Those take A untransposed, so the reduction over the rows of
+// dP needs dP^T (weight n x k) or A^T (weight k x n) laid out once.
+int gemm_epilog_plan_backward(ge_handle h) {
+    if (!h) return GE_ERR_NULL;
+    if (!h->planned || !h->residual) return GE_ERR_STATE;
+    const ge_desc& d = h->d;
+    if (d.a_type != d.d_type || elem_size(d.a_type) < 2) return GE_ERR_DTYPE;
+    const int e = h->epilog;
+    if (e != GE_EPILOG_NONE && e != GE_EPILOG_BIAS && e != GE_EPILOG_RELU_AUX_BIAS && e != GE_EPILOG_GELU_AUX_BIAS)
+        return GE_ERR_EPILOG;
+    const int64_t es = elem_size(d.a_type), per = 16 / es;
+    if (ceil_div(d.m, kGradTile) > 65535) return GE_ERR_SHAPE;
+    ge_plan_s q = *h;
+    const bool act = has_aux(e);   // dP differs from dD
+    q.ld_dp = act ? (int64_t)round_up((size_t)d.n, per) : d.ldd;
+    q.bw_dp = act ? round_up((size_t)d.m * q.ld_dp * es, 256) : 0;
+    q.ld_t = (int64_t)round_up((size_t)d.m, per);
+    const bool kn = d.op_b == GE_OP_N;
+    q.bw_t = round_up((size_t)(kn ? d.k : d.n) * q.ld_t * es, 256);
+    q.bw_part = e == GE_EPILOG_NONE ? 0
+                : round_up((h->axis == GE_BIAS_COL ? (size_t)ceil_div(d.m, kGradTile) * d.n
+                                                   : (size_t)ceil_div(d.n, kGradTile) * d.m) * sizeof(float), 256);
+    // dA: dP (m x n) times B^T; B given n x k is k-major for it (OP_N)
+    const ge_desc da = {d.m, d.k, d.n, d.a_type, d.a_type, d.a_type, d.a_type, kn ? GE_OP_T : GE_OP_N, 0,
+                        q.ld_dp, d.ldb, d.lda};
+    // dB, k x n: A^T (k x m) times dP; n x k: dP^T (n x m) times A
+    const ge_desc db = {kn ? d.k : d.n, kn ? d.n : d.k, d.m, d.a_type, d.a_type, d.a_type, d.a_type, GE_OP_N, 0,
+                        q.ld_t, kn ? q.ld_dp : d.lda, d.ldb};
+    ge_handle ga = nullptr, gb = nullptr;
+    int st = gemm_epilog_create(&ga, &da);
+    if (st == GE_OK) st = gemm_epilog_create(&gb, &db);
+    if (st == GE_OK) st = gemm_epilog_plan(ga, GE_EPILOG_NONE, GE_BIAS_COL, nullptr);
+    if (st == GE_OK) st = gemm_epilog_plan(gb, GE_EPILOG_NONE, GE_BIAS_COL, nullptr);
+    if (st != GE_OK) {
+        gemm_epilog_free(ga);
+        gemm_epilog_free(gb);
+        return st;
+    }
+    size_t wa = 0, wb = 0;
+    gemm_epilog_workspace_size(ga, &wa);
+    gemm_epilog_workspace_size(gb, &wb);
+    q.bw_gemm = wa > wb ? wa : wb;   // the products run one after the other
+    delete q.g_a;
+    delete q.g_b;
+    q.g_a = ga;
+    q.g_b = gb;
+    q.backward = true;
+    *h = q;
+    return GE_OK;
+}
+
+int gemm_epilog_backward_workspace_size(ge_handle h, size_t* bytes) {
+    if (!h || !bytes) return GE_ERR_NULL;
+    if (!h->backward) return GE_ERR_STATE;
+    *bytes = h->bw_dp + h->bw_t + h->bw_part + h->bw_gemm;
+    return GE_OK;
+}
+
+int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void* B, const void* aux, void* dA, void* dB,
+                         void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!h) return GE_ERR_NULL;
+    if (!h->planned || !h->residual || !h->backward) return GE_ERR_STATE;
+    const ge_desc& d = h->d;
+    const int e = h->epilog;
+    const bool kn = d.op_b == GE_OP_N, act = has_aux(e);
+    if ((!dD && d.m * d.n > 0) || (!A && d.m * d.k > 0 && dB) || (!B && d.k * d.n > 0 && dA)) return GE_ERR_NULL;
+    if (aux && !act) return GE_ERR_EPILOG;
+    if (!aux && act && d.m * d.n > 0) return GE_ERR_EPILOG;
+    if (dbias && e == GE_EPILOG_NONE) return GE_ERR_EPILOG;
+    if (!aligned(dD, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(aux, 16) || !aligned(dA, 16) ||
+        !aligned(dB, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
+        return GE_ERR_ALIGN;
+    const size_t need = h->bw_dp + h->bw_t + h->bw_part + h->bw_gemm;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GE_ERR_WORKSPACE;
+    if (test_fail_launch()) return GE_ERR_HIP;
+    uint8_t* ws = (uint8_t*)workspace;
+    uint8_t *w_dp = ws, *w_t = ws + h->bw_dp, *w_part = w_t + h->bw_t, *w_gemm = w_part + h->bw_part;
+    const void* dP = act ? w_dp : dD;
+    const int64_t len = h->axis == GE_BIAS_COL ? d.n : d.m;
+    // a sum over no rows (or columns) is zero; the products write zeros for an empty reduction
+    if (d.m > 0 && d.n > 0 && (act || dbias || (dB && !kn))) {
+        GradArgs g = {};
+        g.src = dD;
+        g.aux = aux;
+        g.dst = act ? w_dp : nullptr;
+        g.dst_t = dB && !kn ? w_t : nullptr;
+        g.partial = dbias ? (float*)w_part : nullptr;
+        g.rows = (int32_t)d.m;
+        g.cols = (int32_t)d.n;
+        g.axis = h->axis;
+        g.ldaux = (int32_t)h->ldaux;
+        g.ld = d.ldd;
+        g.ldd = h->ld_dp;
+        g.ldt = h->ld_t;
+        const int kind = e == GE_EPILOG_RELU_AUX_BIAS ? GRAD_MASK : e == GE_EPILOG_GELU_AUX_BIAS ? GRAD_GELU : GRAD_PLAIN;
+        if (launch_grad_prepare(d.a_type, kind, g, stream) != 0) return GE_ERR_HIP;
+    }
+    if (dbias && len > 0) {
+        KernelArgs z;
+        memset(&z, 0, sizeof(z));
+        z.bias = dbias;
+        z.partial = (float*)w_part;
+        z.m = (int32_t)d.m;
+        z.n = (int32_t)d.n;
+        z.axis = h->axis;
+        z.batch = 1;
+        const int parts = d.m > 0 && d.n > 0 ? (int)ceil_div(h->axis == GE_BIAS_COL ? d.m : d.n, kGradTile) : 0;
+        if (launch_bgrad_reduce(d.a_type, z, parts, stream) != 0) return GE_ERR_HIP;
+    }
+    if (dB && kn && d.m > 0 && d.k > 0) {
+        GradArgs g = {};
+        g.src = A;
+        g.dst_t = w_t;
+        g.rows = (int32_t)d.m;
+        g.cols = (int32_t)d.k;
+        g.axis = GE_BIAS_COL;
+        g.ld = d.lda;
+        g.ldt = h->ld_t;
+        if (launch_grad_prepare(d.a_type, GRAD_COPY, g, stream) != 0) return GE_ERR_HIP;
+    }
+    int st = GE_OK;
+    if (dA)
+        st = gemm_epilog_execute(h->g_a, dP, B, nullptr, dA, nullptr, nullptr, nullptr, h->bw_gemm ? w_gemm : nullptr,
+                                 h->bw_gemm, stream);
+    if (st == GE_OK && dB)
+        st = gemm_epilog_execute(h->g_b, w_t, kn ? dP : A, nullptr, dB, nullptr, nullptr, nullptr,
+                                 h->bw_gemm ? w_gemm : nullptr, h->bw_gemm, stream);
+    return st;
+}
+
 int gemm_epilog_free(ge_handle h) {
+    if (h) {
+        delete h->g_a;
+        delete h->g_b;
+    }
     delete h;
     return GE_OK;
 }
@@ -743,7 +1075,7 @@ int gemm_epilog_autotune(ge_handle h, const void* A, const void* B, const void* 
                          const float* scale_a, const float* scale_b, void* workspace, size_t workspace_bytes,
                          int32_t iters, void* stream, float* best_ms) {
     if (!h) return GE_ERR_NULL;
-    if (!h->planned) return GE_ERR_STATE;
+    if (!h->planned || h->residual) return GE_ERR_STATE;
     if (iters < 1) return GE_ERR_SHAPE;
     const ge_plan_s orig = *h;
     // candidates: tile ids (tile path) or row groups x K splits (small-m
@@ -823,11 +1155,17 @@ int gemm_epilog_describe(ge_handle h, char* buf, size_t cap) {
         snprintf(buf, cap, "m=%lld n=%lld k=%lld unplanned", (long long)d.m, (long long)d.n, (long long)d.k);
         return GE_OK;
     }
-    const TileShape* t = find_tile(h->tile_id);
+    const TileShape* t = h->residual ? find_res_tile(h->tile_id) : find_tile(h->tile_id);
+    if (h->path == PATH_SKINNY) {
+        snprintf(buf, cap, "m=%lld n=%lld k=%lld a=%d d=%d op_b=%d epilog=%d axis=%d path=skinny rows=%d cols=%d grid=%u "
+                 "workspace=0 residual=1", (long long)d.m, (long long)d.n, (long long)d.k, d.a_type, d.d_type, d.op_b,
+                 h->epilog, h->axis, 16 * h->skinny_mb, 16 * h->group_m, h->grid);
+        return GE_OK;
+    }
     snprintf(buf, cap,
              "m=%lld n=%lld k=%lld a=%d d=%d op_b=%d epilog=%d axis=%d path=%s tile=%dx%d waves=%dx%d "
              "tile_id=%d kernel=%d stages=%d grid=%u group_m=%d split_k=%d unfused=%d workspace=%zu "
-             "ldaux_words=%lld k_stagger=%d",
+             "ldaux_words=%lld k_stagger=%d%s",
              (long long)d.m, (long long)d.n, (long long)d.k, d.a_type, d.d_type, d.op_b, h->epilog, h->axis,
              h->path == PATH_SMALLM ? "smallm" : "tile", t ? t->bm : 16, t ? t->bn : 16 * h->group_m, t ? t->wm : 1,
              t ? t->wn : 8, h->tile_id, t ? t->kernel : 0,
@@ -835,7 +1173,7 @@ int gemm_epilog_describe(ge_handle h, char* buf, size_t cap) {
              h->split_k,
              h->unfused,
              h->ws_c + h->ws_partial + h->ws_counters + h->ws_bgrad, (long long)h->ldaux,
-             h->k_stagger);
+             h->k_stagger, h->residual ? " residual=1" : "");
     return GE_OK;
 }
 

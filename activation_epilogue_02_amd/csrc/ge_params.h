@@ -80,8 +80,19 @@ struct MxArgs {
     int64_t bs_sa, bs_sb;
 };
 
+// Second kernel argument of the residual instantiations
+// (gemm_epilog_execute_residual): D = res + act(s * row_scale[i] *
+// col_scale[j] * (A*B)[i][j] + bias).  The block scales (MxArgs) are set for
+// MX operands only.
+struct ResArgs : MxArgs {
+    const void* res;          // D's dtype, row stride ldr elements; NULL = none
+    const float* row_scale;   // m values, NULL = 1
+    const float* col_scale;   // n values, NULL = 1
+    int64_t ldr;
+};
+
 // Kernel families.
-enum Path : int32_t { PATH_TILE = 1, PATH_SMALLM = 2 };
+enum Path : int32_t { PATH_TILE = 1, PATH_SMALLM = 2, PATH_SKINNY = 3 };
 
 // Tile shapes of the MFMA tile kernels: block tile BM x BN, waves WM x WN.
 // Kernel 1 (tile_kernel.h): register-staged, two LDS stages, every dtype.
@@ -118,6 +129,21 @@ constexpr TileShape kTiles[kNumTiles] = {
     {16, 256, 256, 2, 4, 6, 4},  // fp8 only: 8 waves, 128 x 64 per wave, 64-byte K steps
 };
 
+// Tiles of the residual product (launch_tile_res): the shapes above with an
+// epilogue of their own, and two split-K ones for 8-bit inputs (ids 17, 18).
+constexpr int kNumResTiles = 9;
+constexpr TileShape kResTiles[kNumResTiles] = {
+    {1, 64, 64, 2, 2, 1, 2},     // fp32
+    {2, 128, 128, 2, 2, 1, 2},   // fp32
+    {6, 256, 256, 2, 4, 2, 4},   // 16-bit
+    {8, 128, 128, 2, 2, 2, 4},   // 16-bit, fp8
+    {14, 64, 64, 2, 2, 5, 4},    // 16-bit, split-K
+    {15, 256, 128, 4, 2, 2, 4},  // fp8
+    {16, 256, 256, 2, 4, 6, 4},  // fp8, 64-byte K steps
+    {17, 64, 128, 2, 2, 5, 4},   // fp8, split-K
+    {18, 128, 128, 2, 2, 5, 4},  // block-scaled fp8, split-K
+};
+
 // LDS stages the pipelined kernel uses: a stage holds BM + BN rows of 64
 // bytes (16-bit inputs in kernel 2; fp8 in kernel 6) or 128 bytes (fp8 in
 // kernel 2, 16-bit inputs in kernels 4 and 5); at most 160 KiB in total.
@@ -134,6 +160,14 @@ int launch_tile(int tile_id, int a_type, int d_type, int op_b, const KernelArgs&
 // scales).  Returns a hipError_t.
 int launch_tile_mx(int tile_id, int d_type, int op_b, const KernelArgs& args, const MxArgs& mx,
                    unsigned grid, void* stream);
+
+// Launch a residual product: a tile of kResTiles, or the streaming kernel for
+// few rows with mb (1, 2 or 4) groups of 16 rows of A and rg (1 or 2) of
+// 16 columns of D per workgroup.  mx: block-scaled operands.  Returns a hipError_t.
+int launch_tile_res(int tile_id, int a_type, int d_type, int op_b, const KernelArgs& args, const ResArgs& res,
+                    unsigned grid, void* stream);
+int launch_skinny(int a_type, int d_type, int mb, int rg, const KernelArgs& args, const ResArgs& res, unsigned grid,
+                  void* stream);
 
 // Launch the small-m streaming kernel with rg (1, 2 or 4) groups of 16 W
 // rows per wave; args.tiles_n counts column blocks of 16 * rg rows.

@@ -1,0 +1,9 @@
+// res_mx_f32.hip -- the residual product's tiles for block-scaled fp8 inputs and
+// fp32 output.
+#include "tile2_kernel.h"
+
+namespace ge {
+
+ResFn pick_res_mx_f32(int op_b, int tile_id) { return pick_res_op<GE_MXF8_E4M3, GE_F32>(op_b, tile_id); }
+
+}  // namespace ge

@@ -160,9 +160,12 @@ __device__ __forceinline__ int swz_row(int row) {
 // Its body stays in the __global__ function itself: moved into a force-inlined
 // device function, the same code compiled to 3x the scalar-register spills
 // and 768 bytes of scratch per lane on the 256 x 256 tile (10x slower).
+// RES: the residual product's instantiations, with the epilogue of
+// res_epilogue.h and its further arguments.
 template <int DIN, int DOUT, int OPB, int BM, int BN, int WM, int WN, int S, bool REG, int RB, bool SPLIT = false,
-          bool MX = false>
-__global__ void __launch_bounds__(WM* WN * 64) ge_tile2_kernel(KernelArgs p_all, MxArgs mx_all) {
+          bool MX = false, bool RES = false>
+__global__ void __launch_bounds__(WM* WN * 64)
+    ge_tile2_kernel(KernelArgs p_all, typename std::conditional<RES, ResArgs, MxArgs>::type mx_all) {
     const KernelArgs p = batch_slice(p_all, blockIdx.y);   // this product of a batch
     using C = Tile2Cfg<DIN, DOUT, OPB, BM, BN, WM, WN, S, REG, RB, MX>;
     constexpr int BK = C::BK, SE = C::SE, ESZ = C::ESZ, EPC = C::EPC;
@@ -255,8 +258,9 @@ __global__ void __launch_bounds__(WM* WN * 64) ge_tile2_kernel(KernelArgs p_all,
     const uint8_t* srcSA[C::SCA > 0 ? C::SCA : 1];
     const uint8_t* srcSB[C::SCB > 0 ? C::SCB : 1];
     if constexpr (MX) {
-        const uint8_t* sa = mx_all.sa + (int64_t)blockIdx.y * mx_all.bs_sa;
-        const uint8_t* sb = mx_all.sb + (int64_t)blockIdx.y * mx_all.bs_sb;
+        // (a K slice starts at a multiple of 128 K values: whole scale words)
+        const uint8_t* sa = mx_all.sa + (int64_t)blockIdx.y * mx_all.bs_sa + (SPLIT ? ks / 32 : 0);
+        const uint8_t* sb = mx_all.sb + (int64_t)blockIdx.y * mx_all.bs_sb + (SPLIT ? ks / 32 : 0);
 #pragma unroll
         for (int c = 0; c < C::SCA; ++c)
             srcSA[c] = sa + (int64_t)min(m0 + wm * C::TM + 64 * c + lane, max(M - 1, 0)) * mx_all.ld;
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(WM* WN * 64) ge_tile2_kernel(KernelArgs p_all,
             uint32_t keep = 0u;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (4 * t + j < mx_all.kb) keep |= 0xffu << (8 * j);
+                if (4 * t + j + (SPLIT ? ks / 32 : 0) < mx_all.kb) keep |= 0xffu << (8 * j);
 #pragma unroll
             for (int sc = 0; sc < C::SCA + C::SCB; ++sc) {
                 const uint8_t* src = sc < C::SCA ? srcSA[sc] : srcSB[sc - C::SCA];
@@ -902,6 +906,11 @@ __global__ void __launch_bounds__(WM* WN * 64) ge_tile2_kernel(KernelArgs p_all,
         }
     }
 
+    if constexpr (RES) {
+        res_epilogue<DOUT, C::FM, C::FN, BN, C::NT>(p, mx_all, acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, tn, lane,
+                                                   tid);
+        return;
+    } else {
     // ---- fused epilogue on the accumulators (as in tile_kernel.h) ----
     // the product's scale: fp8 dequantisation factors, or an alpha for any dtype
     float s = 1.0f;
@@ -1090,6 +1099,7 @@ __global__ void __launch_bounds__(WM* WN * 64) ge_tile2_kernel(KernelArgs p_all,
             }
         }
     }
+    }   // RES
 }
 
 
@@ -1106,6 +1116,29 @@ Tile2Fn pick_tile2_mx(int tile_id) {
 template <int DOUT>
 Tile2Fn pick_op2_mx(int op_b, int tile_id) {
     return op_b == GE_OP_T ? pick_tile2_mx<DOUT, GE_OP_T>(tile_id) : pick_tile2_mx<DOUT, GE_OP_N>(tile_id);
+}
+
+// The residual product's tiles (kResTiles).
+template <int DIN, int DOUT, int OPB>
+ResFn pick_res_tile(int tile_id) {
+    if constexpr (DIN == GE_MXF8_E4M3) {
+        if (tile_id == 18) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, true, true, true>;
+    } else if constexpr (DIN == GE_F8_E4M3) {
+        if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, true>;
+        if (tile_id == 15) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 128, 4, 2, 4, false, 64, false, false, true>;
+        if (tile_id == 16) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 256, 2, 4, 4, false, 32, false, false, true>;
+        if (tile_id == 17) return ge_tile2_kernel<DIN, DOUT, OPB, 64, 128, 2, 2, 4, false, 64, true, false, true>;
+    } else {
+        if (tile_id == 6) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 256, 2, 4, 4, false, 64, false, false, true>;
+        if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, true>;
+        if (tile_id == 14) return ge_tile2_kernel<DIN, DOUT, OPB, 64, 64, 2, 2, 4, false, 128, true, false, true>;
+    }
+    return nullptr;
+}
+
+template <int DIN, int DOUT>
+ResFn pick_res_op(int op_b, int tile_id) {
+    return op_b == GE_OP_T ? pick_res_tile<DIN, DOUT, GE_OP_T>(tile_id) : pick_res_tile<DIN, DOUT, GE_OP_N>(tile_id);
 }
 
 template <int DIN, int DOUT, int OPB>

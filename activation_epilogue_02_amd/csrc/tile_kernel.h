@@ -33,7 +33,7 @@
 //    XCDs (round-robin), so ids are remapped to give each XCD a contiguous
 //    range of tiles, traversed in groups of `group_m` tile-rows for L2 reuse.
 #pragma once
-#include "ge_device.h"
+#include "res_epilogue.h"
 
 namespace ge {
 
@@ -107,9 +107,11 @@ __device__ __forceinline__ void tile_coords(const KernelArgs& p, int& tm, int& t
     tn = r / gm;
 }
 
-template <int DIN, int DOUT, int OPB, int BM, int BN, int WM, int WN>
+// (RES...: empty, or ResArgs for the residual product, whose epilogue is
+// res_epilogue.h's)
+template <int DIN, int DOUT, int OPB, int BM, int BN, int WM, int WN, typename... RES>
 __global__ void __launch_bounds__(WM* WN * 64)
-ge_tile_kernel(KernelArgs p_all) {
+ge_tile_kernel(KernelArgs p_all, RES... res) {
     const KernelArgs p = batch_slice(p_all, blockIdx.y);   // this product of a batch
     using C = TileCfg<DIN, DOUT, OPB, BM, BN, WM, WN>;
     constexpr int ESZ = C::ESZ, BK = C::BK, E = C::E, NT = C::NT;
@@ -318,6 +320,11 @@ ge_tile_kernel(KernelArgs p_all) {
         __syncthreads();
     }
 
+    if constexpr (sizeof...(RES) == 1) {
+        res_epilogue<DOUT, C::FM, C::FN, BN, NT>(p, res..., acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, tn, lane,
+                                                tid);
+        return;
+    } else {
     // ---- fused epilogue on the accumulators ----
     // the product's scale: fp8 dequantisation factors, or an alpha for any dtype
     float s = 1.0f;
@@ -431,6 +438,7 @@ ge_tile_kernel(KernelArgs p_all) {
             }
         }
     }
+    }   // RES
 }
 
 typedef void (*TileFn)(KernelArgs);
@@ -473,5 +481,18 @@ Tile2Fn pick_tile2_bf16_f8(int op_b, int tile_id);   // fp8 (E4M3) output
 Tile2Fn pick_tile2_f16_f8(int op_b, int tile_id);
 Tile2Fn pick_tile2_f8_f8(int op_b, int tile_id);
 Tile2Fn pick_tile2_mx_f8_f8(int op_b, int tile_id);
+// the residual product's instantiations, one table per dtype pair
+typedef void (*ResFn)(KernelArgs, ResArgs);
+ResFn pick_res_f32_f32(int op_b, int tile_id);
+ResFn pick_res_f16_f16(int op_b, int tile_id);
+ResFn pick_res_f16_f32(int op_b, int tile_id);
+ResFn pick_res_bf16_bf16(int op_b, int tile_id);
+ResFn pick_res_bf16_f32(int op_b, int tile_id);
+ResFn pick_res_f8_bf16(int op_b, int tile_id);
+ResFn pick_res_f8_f16(int op_b, int tile_id);
+ResFn pick_res_f8_f32(int op_b, int tile_id);
+ResFn pick_res_mx_bf16(int op_b, int tile_id);
+ResFn pick_res_mx_f16(int op_b, int tile_id);
+ResFn pick_res_mx_f32(int op_b, int tile_id);
 
 }  // namespace ge

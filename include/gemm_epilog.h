@@ -418,6 +418,63 @@ int gemm_epilog_execute_mx(ge_handle h, const void* A, const void* B, const void
                            const float* scale_a, const float* scale_b, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* ---- residual product -----------------------------------------------------
+ *   P = s * row_scale[i] * col_scale[j] * (A*B)[i][j] + bias
+ *   D = R + act(P)
+ * The last product of a transformer block: the residual stream R is added
+ * after the activation (execute_c adds its term before it), and 8-bit operands
+ * with one scale per row of A (a token's, ge_rms_norm.h makes them) and per
+ * column of B (a weight channel's) are scaled in the same epilogue.
+ *
+ * gemm_epilog_plan_residual plans the handle for it (and for it alone:
+ * execute and its other forms return GE_ERR_STATE until gemm_epilog_plan).
+ * Epilogues: NONE, BIAS, RELU_BIAS, RELU_AUX_BIAS, GELU_BIAS, GELU_AUX_BIAS,
+ * TANH_BIAS; aux holds the mask of, or, P (before the residual).  Types: every
+ * combination of ge_desc but an E4M3 D; one product (batch 0 or 1).
+ * workspace_size, aux_ld and describe then answer for this plan.
+ * Errors: GE_ERR_NULL; GE_ERR_EPILOG (another epilogue or axis); GE_ERR_SHAPE
+ * (a batch, or a tile whose rows span 4 GiB or more); GE_ERR_DTYPE (E4M3 D).
+ *
+ * gemm_epilog_execute_residual launches it for m rows, 0 <= m <= the planned.
+ *   a_scales, b_scales   block scales of GE_MXF8_E4M3 operands (see
+ *                        execute_mx), NULL for every other type
+ *   residual, ldr        R, m x n in D's type with row stride ldr elements;
+ *                        NULL = 0.  R may be D itself (each value is read
+ *                        before it is written, by the same thread).
+ *   row_scale, col_scale device fp32, m and n values; NULL = 1.  Any type.
+ *   the others           as for execute
+ * Alignment as for execute; col_scale 16 bytes, row_scale 4.
+ * Errors: those of execute; GE_ERR_STATE (not planned for it); GE_ERR_SHAPE
+ * (m, or ldr < n); GE_ERR_DTYPE (block scales for a type without). */
+int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis);
+int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const void* B, const void* a_scales,
+                                 const void* b_scales, const void* bias, const void* residual, int64_t ldr,
+                                 const float* row_scale, const float* col_scale, const float* scale_a,
+                                 const float* scale_b, void* D, void* aux, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Backward pass of the residual product, for the planned m rows and without
+ * scales (training runs in 16 or 32 bits):
+ *   dP = dD * act'(aux)          (RELU_AUX_BIAS, GELU_AUX_BIAS; else dP = dD)
+ *   dA = dP B^T,  dB = A^T dP in B's own layout,  dbias = sums of dP
+ *   (the residual's gradient is dD itself)
+ * gemm_epilog_plan_backward follows plan_residual with NONE, BIAS,
+ * RELU_AUX_BIAS or GELU_AUX_BIAS (the epilogues that keep what the gradient
+ * needs; others: GE_ERR_EPILOG) and a_type == d_type of 16 or 32 bits (others:
+ * GE_ERR_DTYPE).  backward takes dD with D's layout (ldd), A and B as the
+ * forward had them, aux as it wrote it; dA has A's layout (lda) and dB B's
+ * (ldb).  dA, dB and dbias may each be NULL when not wanted.  dP is rounded
+ * to the operands' type before the products (they take 16-bit operands), once;
+ * dbias sums the fp32 values.  Sums have a fixed order: equal calls give equal
+ * bits.  The outputs must not overlap the inputs.
+ * Errors: GE_ERR_NULL, GE_ERR_STATE (not planned), GE_ERR_EPILOG (aux given or
+ * missing, dbias for NONE), GE_ERR_ALIGN, GE_ERR_WORKSPACE, GE_ERR_HIP; at
+ * plan also those of create and plan for the two products. */
+int gemm_epilog_plan_backward(ge_handle h);
+int gemm_epilog_backward_workspace_size(ge_handle h, size_t* bytes);
+int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void* B, const void* aux, void* dA, void* dB,
+                         void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Release the handle (NULL is accepted).  Host-only. */
 int gemm_epilog_free(ge_handle h);
 
