@@ -138,15 +138,16 @@ def _check(status: int, what: str):
 def _ptr(x) -> Optional[int]:
     if x is None:
         return None
-    if isinstance(x, torch.Tensor):
-        return x.data_ptr()
-    return int(x)
+    return x.data_ptr() if isinstance(x, torch.Tensor) else int(x)
 
 
 def _stream(stream) -> Optional[int]:
     """The handle of a torch stream (default: the current one), or a raw one."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        # the handle alone (0.2 us; a stream object takes 2.8 us, as long as a small kernel);
+        # before torch has set up the GPU only the default stream can be current
+        return (torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if torch.cuda.is_initialized()
+                else None)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 

@@ -128,20 +128,31 @@ const TileShape* find_res_tile(int id) {
     return nullptr;
 }
 
-// The residual product's tile: the largest that gives the CUs work, and below
-// that the smallest, which splits K.
+// The residual product's tile: the largest that gives every CU a tile, and
+// below that the smallest, which splits K.  Measured (bias, residual, bf16
+// output; us):
+//   bf16 256 x 256 / 128 x 128: 4096 x 4096 x 4096 (256 large tiles) 149 / 191,
+//     2048 x 4096 x 4096 (128) 89 / 89, 3000 x 2000 x 700 (96) 29 / 23;
+//   bf16 128 x 128 / 64 x 64: 2048 x 4096 x 4096 (512) 89 / 101, 3000 x 2000 x 700
+//     (384) 23 / 24, 512 x 4096 x 4096 (128) 37 / 33, 1000 x 1000 x 1000 (64) 21 / 10;
+//   E4M3 256 x 128 / 128 x 128 / 64 x 128 split-K: 2048 x 4096 x 4096 (256 of the
+//     first) 41 / 48 / 60, 1024 x 4096 x 4096 (128) 33 / 25 / 33, 500 x 2000 x 2000
+//     25 / 19 / 14; 256 x 256 and 256 x 128 at 8192 x 4096 x 16384: 472 / 470;
+//   block-scaled 128 x 128 with two workgroups per CU / one with four stages and
+//     split-K: 8192 x 8192 x 8192 758 / 875, 1300 x 4096 x 4096 (352) 53 / 60,
+//     1024 x 4096 x 4096 (256) 38 / 34.
 int choose_res_tile(const ge_desc& d) {
     const int64_t t256 = ceil_div(d.m, 256) * ceil_div(d.n, 256);
     const int64_t t128 = ceil_div(d.m, 128) * ceil_div(d.n, 128);
     switch (d.a_type) {
     case GE_F32: return t128 >= 256 ? 2 : 1;
-    case GE_MXF8_E4M3: return 18;
+    case GE_MXF8_E4M3: return t128 > 256 ? 19 : 18;
     case GE_F8_E4M3:
         if (t256 >= 512) return 16;
-        if (ceil_div(d.m, 256) * ceil_div(d.n, 128) >= 512) return 15;
+        if (ceil_div(d.m, 256) * ceil_div(d.n, 128) >= 256) return 15;
         return t128 >= 256 ? 8 : 17;
     }
-    if (t256 >= 512) return 6;
+    if (t256 >= 256) return 6;
     return t128 >= 256 ? 8 : 14;
 }
 

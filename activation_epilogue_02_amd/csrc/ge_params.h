@@ -130,8 +130,8 @@ constexpr TileShape kTiles[kNumTiles] = {
 };
 
 // Tiles of the residual product (launch_tile_res): the shapes above with an
-// epilogue of their own, and two split-K ones for 8-bit inputs (ids 17, 18).
-constexpr int kNumResTiles = 9;
+// epilogue of their own, and three for 8-bit inputs (ids 17 to 19).
+constexpr int kNumResTiles = 10;
 constexpr TileShape kResTiles[kNumResTiles] = {
     {1, 64, 64, 2, 2, 1, 2},     // fp32
     {2, 128, 128, 2, 2, 1, 2},   // fp32
@@ -142,6 +142,7 @@ constexpr TileShape kResTiles[kNumResTiles] = {
     {16, 256, 256, 2, 4, 6, 4},  // fp8, 64-byte K steps
     {17, 64, 128, 2, 2, 5, 4},   // fp8, split-K
     {18, 128, 128, 2, 2, 5, 4},  // block-scaled fp8, split-K
+    {19, 128, 128, 2, 2, 2, 2},  // block-scaled fp8, two workgroups per CU
 };
 
 // LDS stages the pipelined kernel uses: a stage holds BM + BN rows of 64

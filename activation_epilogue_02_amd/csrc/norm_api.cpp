@@ -25,21 +25,19 @@ NormShape pick_shape(const NormShape (&table)[N], int64_t chunks) {
     return kNormLong;
 }
 
-int rows_per_block(const NormShape& s) { return s.threads == 64 ? 4 : 1; }
-
-// Workgroups of a backward launch: each walks rows blockIdx, blockIdx +
-// blocks, ... and keeps its share of dgamma in registers, so fewer blocks
-// mean fewer partial sums to write and read again, and more blocks more loads
-// in flight.  Four 256-thread workgroups (or their threads) per CU.
-int64_t backward_blocks(const NormShape& s, int64_t rows) {
-    const int64_t threads = s.threads == 64 ? 256 : s.threads;
-    const int64_t most = 256 * (1024 / threads);
-    const int64_t need = ceil_div(rows, rows_per_block(s));
-    return need < most ? need : most;
+// Workgroups of a forward launch: one per row (per four of the one-wave
+// shapes), up to a grid that the runtime takes; beyond it they walk the rows.
+int64_t forward_blocks(const NormShape& s, int64_t rows) {
+    const int64_t need = s.threads == 64 ? ceil_div(rows, 4) : rows;
+    return need < 1 << 20 ? need : 1 << 20;
 }
 
+// Of a backward launch: one per CU, each walking rows blockIdx, blockIdx +
+// blocks, ... (see norm_bwd).
+int64_t backward_blocks(int64_t rows) { return rows < 256 ? rows : 256; }
+
 size_t partial_bytes(const ge_norm_s& h, int64_t rows) {
-    return round_up((size_t)backward_blocks(h.bwd, rows) * (size_t)h.d.cols * sizeof(float), 256);
+    return round_up((size_t)backward_blocks(rows) * (size_t)h.d.cols * sizeof(float), 256);
 }
 
 }  // namespace
@@ -101,6 +99,7 @@ int ge_rms_norm_forward(ge_norm_handle h, int64_t rows, const void* x, const voi
     a.rstd = rstd;
     a.rows = (int32_t)rows;
     a.cols = (int32_t)d.cols;
+    a.blocks = (int32_t)forward_blocks(h->fwd, rows);
     a.lds = (int32_t)GE_MX_SCALE_LD(d.cols);
     a.ld = d.ld;
     a.ldy = d.ldy;
@@ -132,7 +131,7 @@ int ge_rms_norm_backward(ge_norm_handle h, int64_t rows, const void* dy, const v
     a.partial = dgamma ? (float*)workspace : nullptr;
     a.rows = (int32_t)rows;
     a.cols = (int32_t)d.cols;
-    a.blocks = (int32_t)backward_blocks(h->bwd, rows);
+    a.blocks = (int32_t)backward_blocks(rows);
     a.ld = d.ld;
     a.eps = d.eps;
     a.inv_cols = (float)(1.0 / (double)d.cols);
@@ -146,7 +145,7 @@ int ge_rms_norm_describe(ge_norm_handle h, char* buf, size_t cap) {
     if (cap == 0) return GE_OK;
     snprintf(buf, cap, "rows=%lld cols=%lld type=%d out=%d forward=%dx%d backward=%dx%d blocks=%lld",
              (long long)h->d.rows, (long long)h->d.cols, h->d.type, h->d.out, h->fwd.threads, h->fwd.chunks,
-             h->bwd.threads, h->bwd.chunks, (long long)backward_blocks(h->bwd, h->d.rows));
+             h->bwd.threads, h->bwd.chunks, (long long)backward_blocks(h->d.rows));
     return GE_OK;
 }
 

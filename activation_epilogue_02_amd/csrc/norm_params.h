@@ -23,7 +23,7 @@ struct NormArgs {
     void* dgamma;        // or NULL
     float* partial;      // backward: blocks x cols fp32
     int32_t rows, cols;
-    int32_t blocks;      // backward: workgroups of the launch
+    int32_t blocks;      // workgroups of the launch
     int32_t lds;         // MX: bytes per row of scales
     int64_t ld, ldy;
     float eps, inv_cols;
@@ -34,8 +34,8 @@ struct NormArgs {
 struct NormShape {
     int32_t threads, chunks;
 };
-constexpr NormShape kNormFwd[] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
-constexpr NormShape kNormBwd[] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2}, {1024, 2}, {1024, 4}};
+constexpr NormShape kNormFwd[] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 3}, {256, 4}, {1024, 2}, {1024, 4}};
+constexpr NormShape kNormBwd[] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 3}, {512, 2}, {512, 3}, {1024, 2}, {1024, 4}};
 constexpr NormShape kNormLong = {1024, 0};
 
 int launch_norm_forward(int type, int out, NormShape s, const NormArgs& a, void* stream);

@@ -7,19 +7,24 @@
 // a row and their sums meet in LDS in wave order, so no partial sum leaves
 // the CU and the call is one launch without a workspace: an exchange between
 // workgroups costs about 6 us, as long as 30 MB of W take to stream.
-//  * W goes from memory to the matrix instruction's operand registers
-//    directly: lane (r = lane % 16, q = lane / 16) takes the 16-byte chunks q
-//    and 4 + q of row r's span, which are its K values in the 16x16x32
+//  * A load instruction takes whole 128-byte lines (lane l: row l / 8, chunk
+//    l % 8): fetched in the operand layout (lane: row l % 16, chunk l / 16) an
+//    instruction touches 16 half lines, and the 16 x 4096 x 16384 bf16 product
+//    took 43 us.  Each wave turns a span to the operand layout through 2 KB of LDS
+//    per 16 rows of its own (no barrier), chunks XOR-swizzled by row / 2, so that
+//    neither side meets a bank conflict: lane (r = lane % 16, q = lane / 16)
+//    reads chunks q and 4 + q of row r, which are its K values in the 16x16x32
 //    instruction (two of them per span) and in the 16x16x128 one (one per
 //    span; its four 32-value blocks are the chunk pairs, so lane q's block
 //    scale is byte q of the row's scale word).
-//  * A wave's loads of U spans all go out before its first MFMA, so the
-//    memory latency is paid once per batch.
-//  * x (m rows, read by every workgroup from L2) takes the same pattern.
+//  * U spans are in flight in registers at all times: a span's slot is
+//    loaded again as soon as its bytes are in LDS.
+//  * x (m rows, read by every workgroup from L2) takes the same path.
+//  * Workgroups start at different spans of their waves' K ranges: the rows of
+//    W are often a power of two apart, and in lock-step all of them would ask the
+//    same few memory channels.
 //  * The epilogue's operands (bias, scales, residual) are fetched before
 //    the K loop, so that their latency hides under it.
-#include <type_traits>
-
 #include "ge_device.h"
 
 namespace ge {
@@ -80,7 +85,10 @@ __global__ void __launch_bounds__(kWaves * 64) ge_skinny_kernel(KernelArgs p, Re
     constexpr int ESZ = DIN == GE_F16 || DIN == GE_BF16 ? 2 : 1;
     constexpr int NB = MB * RG;   // 16 x 16 blocks of D
     static_assert(NB <= kWaves, "one block per wave in the epilogue");
-    __shared__ f32x4 red[kWaves][NB][64];
+    constexpr int TILES = RG + MB;   // 16-row groups of W, then of x
+    constexpr int STAGE = kWaves * TILES * 2048, RED = kWaves * NB * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[STAGE > RED ? STAGE : RED];
+    f32x4(*red)[NB][64] = (f32x4(*)[NB][64])smem;   // the waves' sums, after the K loop
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int nblk = blockIdx.x, n0 = nblk * 16 * RG;
@@ -94,21 +102,21 @@ __global__ void __launch_bounds__(kWaves * 64) ge_skinny_kernel(KernelArgs p, Re
     const int s_full = min(s_end, full);
 
     // rows beyond n (W) or m (x) feed outputs that are never stored: clamped
-    const uint8_t* wrow[RG];
-    const uint8_t* xrow[MB];
-    const uint8_t* wsc[RG];
-    const uint8_t* xsc[MB];
+    auto row_of = [&](int tile, int row) __attribute__((always_inline)) {
+        if (tile < RG) return (const uint8_t*)p.B + (int64_t)min(n0 + 16 * tile + row, N - 1) * p.ldb * ESZ;
+        return (const uint8_t*)p.A + (int64_t)min(16 * (tile - RG) + row, M - 1) * p.lda * ESZ;
+    };
+    auto scales_of = [&](int tile) __attribute__((always_inline)) {
+        if (tile < RG) return a.sb + (int64_t)min(n0 + 16 * tile + r, N - 1) * a.ld;
+        return a.sa + (int64_t)min(16 * (tile - RG) + r, M - 1) * a.ld;
+    };
+    const uint8_t* src[TILES][2];   // this lane's rows of the loads
+    const uint8_t* sc[TILES];
 #pragma unroll
-    for (int g = 0; g < RG; ++g) {
-        const int64_t n = min(n0 + 16 * g + r, N - 1);
-        wrow[g] = (const uint8_t*)p.B + n * p.ldb * ESZ;
-        wsc[g] = MX ? a.sb + n * a.ld : nullptr;
-    }
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
-        const int64_t m = min(16 * b + r, M - 1);
-        xrow[b] = (const uint8_t*)p.A + m * p.lda * ESZ;
-        xsc[b] = MX ? a.sa + m * a.ld : nullptr;
+    for (int i = 0; i < TILES; ++i) {
+        src[i][0] = row_of(i, lane >> 3) + 16 * (lane & 7);
+        src[i][1] = row_of(i, 8 + (lane >> 3)) + 16 * (lane & 7);
+        sc[i] = MX ? scales_of(i) : nullptr;
     }
 
     // this wave's block of the epilogue (the waves past NB repeat the last
@@ -143,48 +151,80 @@ __global__ void __launch_bounds__(kWaves * 64) ge_skinny_kernel(KernelArgs p, Re
 #pragma unroll
         for (int b = 0; b < MB; ++b) acc[g][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    int s0 = s_begin;
-    auto batch = [&](auto u_const) __attribute__((always_inline)) {
-        constexpr int U = decltype(u_const)::value;
-        u32x4 w0[U][RG], w1[U][RG], x0[U][MB], x1[U][MB];
-        uint32_t sw[U][RG], sx[U][MB];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t off = (int64_t)(s0 + u) * 128 + 16 * q;
-#pragma unroll
-            for (int g = 0; g < RG; ++g) {
-                w0[u][g] = __builtin_nontemporal_load((const u32x4*)(wrow[g] + off));
-                w1[u][g] = __builtin_nontemporal_load((const u32x4*)(wrow[g] + off + 64));
-                if constexpr (MX) sw[u][g] = *(const uint32_t*)(wsc[g] + 4 * (s0 + u));
-            }
-#pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                x0[u][b] = *(const u32x4*)(xrow[b] + off);
-                x1[u][b] = *(const u32x4*)(xrow[b] + off + 64);
-                if constexpr (MX) sx[u][b] = *(const uint32_t*)(xsc[b] + 4 * (s0 + u));
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int g = 0; g < RG; ++g)
-#pragma unroll
-                for (int b = 0; b < MB; ++b)
-                    acc[g][b] = span_mfma<DIN>(w0[u][g], w1[u][g], x0[u][b], x1[u][b], MX ? sw[u][g] >> (8 * q) : 0u,
-                                               MX ? sx[u][b] >> (8 * q) : 0u, acc[g][b]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        s0 += U;
+    // spans in flight: what 256 registers per lane hold beside the rest
+    constexpr int U = MX ? (TILES <= 2 ? 4 : TILES <= 4 ? 2 : 1) : TILES <= 2 ? 8 : TILES <= 3 ? 6 : TILES <= 5 ? 4 : 2;
+    struct Slot {
+        u32x4 v[TILES][2];
+        uint32_t sc[TILES];
     };
-    // spans per batch: about 128 registers of operands
-    constexpr int U = MB + RG <= 2 ? 8 : MB + RG <= 4 ? 4 : 2;
-    while (s0 + U <= s_full) batch(std::integral_constant<int, U>{});
-    if constexpr (U > 4)
-        if (s0 + 4 <= s_full) batch(std::integral_constant<int, 4>{});
-    if constexpr (U > 2)
-        if (s0 + 2 <= s_full) batch(std::integral_constant<int, 2>{});
-    if (s0 < s_full) batch(std::integral_constant<int, 1>{});
+    uint8_t* st = smem + wave * (TILES * 2048);
+    const int put0 = (lane >> 3) * 128 + (((lane & 7) ^ ((lane >> 4) & 7)) << 4);         // row lane / 8
+    const int put1 = (8 + (lane >> 3)) * 128 + (((lane & 7) ^ (4 + (lane >> 4))) << 4);   // row 8 + lane / 8
+    const int get0 = r * 128 + ((q ^ (r >> 1)) << 4), get1 = r * 128 + (((4 + q) ^ (r >> 1)) << 4);
+    const int count = s_full - s_begin;
+    const int rot = count > 0 ? nblk % count : 0;
+    auto load = [&](Slot& t, int i) __attribute__((always_inline)) {   // full span i of this wave
+        int s = s_begin + i + rot;
+        if (s >= s_full) s -= count;
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x4* g = (const u32x4*)(src[k][j] + (int64_t)s * 128);
+                t.v[k][j] = k < RG ? __builtin_nontemporal_load(g) : *g;
+            }
+            if constexpr (MX) t.sc[k] = *(const uint32_t*)(sc[k] + 4 * s);
+        }
+    };
+    // the slot's span through LDS, its next span's loads (where `more`), its MFMAs
+    auto take = [&](Slot& t, int next, bool more) __attribute__((always_inline)) {
+        uint32_t w[TILES];
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+            *(u32x4*)(st + k * 2048 + put0) = t.v[k][0];
+            *(u32x4*)(st + k * 2048 + put1) = t.v[k][1];
+            w[k] = MX ? t.sc[k] >> (8 * q) : 0u;
+        }
+        // (a wave's LDS operations keep their order: only the compiler must not move them)
+        asm volatile("" ::: "memory");
+        if (more) load(t, next);
+        u32x4 f[TILES][2];
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+            f[k][0] = *(const u32x4*)(st + k * 2048 + get0);
+            f[k][1] = *(const u32x4*)(st + k * 2048 + get1);
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+                acc[g][b] = span_mfma<DIN>(f[g][0], f[g][1], f[RG + b][0], f[RG + b][1], w[g], w[RG + b], acc[g][b]);
+    };
+    if (count > 0) {
+        Slot t[U];
+        if (count >= U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) load(t[u], u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < count) load(t[u], u);
+        }
+        int i = 0;
+        for (; i + 2 * U <= count; i += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) take(t[u], i + U + u, true);
+        }
+        // fewer than 2 U are left
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < count) take(t[u], i + U + u, i + U + u < count);
+        i += U;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < count) take(t[u], 0, false);
+    }
     if (full >= s_begin && full < s_end) {
         // the ragged last span: what lies beyond k is zero in both operands
         // (0 * NaN would not vanish), and its block scales are 1
@@ -194,23 +234,22 @@ __global__ void __launch_bounds__(kWaves * 64) ge_skinny_kernel(KernelArgs p, Re
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (j < blocks) keep |= 0xffu << (8 * j);
-        u32x4 w0[RG], w1[RG];
-        uint32_t sw[RG];
+        u32x4 f[TILES][2];
+        uint32_t w[TILES];
 #pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            w0[g] = chunk_masked<ESZ>(wrow[g], off, bytes);
-            w1[g] = chunk_masked<ESZ>(wrow[g], off + 64, bytes);
-            sw[g] = MX ? (*(const uint32_t*)(wsc[g] + 4 * full) & keep) | (0x7f7f7f7fu & ~keep) : 0u;
+        for (int k = 0; k < TILES; ++k) {
+            const uint8_t* row = row_of(k, r);
+            f[k][0] = chunk_masked<ESZ>(row, off, bytes);
+            f[k][1] = chunk_masked<ESZ>(row, off + 64, bytes);
+            w[k] = MX ? ((*(const uint32_t*)(sc[k] + 4 * full) & keep) | (0x7f7f7f7fu & ~keep)) >> (8 * q) : 0u;
         }
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            const u32x4 x0 = chunk_masked<ESZ>(xrow[b], off, bytes), x1 = chunk_masked<ESZ>(xrow[b], off + 64, bytes);
-            const uint32_t sx = MX ? (*(const uint32_t*)(xsc[b] + 4 * full) & keep) | (0x7f7f7f7fu & ~keep) : 0u;
+        for (int g = 0; g < RG; ++g)
 #pragma unroll
-            for (int g = 0; g < RG; ++g)
-                acc[g][b] = span_mfma<DIN>(w0[g], w1[g], x0, x1, sw[g] >> (8 * q), sx >> (8 * q), acc[g][b]);
-        }
+            for (int b = 0; b < MB; ++b)
+                acc[g][b] = span_mfma<DIN>(f[g][0], f[g][1], f[RG + b][0], f[RG + b][1], w[g], w[RG + b], acc[g][b]);
     }
+    __syncthreads();   // `red` lies over the waves' stages
 #pragma unroll
     for (int g = 0; g < RG; ++g)
 #pragma unroll

@@ -824,10 +824,16 @@ __global__ void __launch_bounds__(WM* WN * 64)
             interleave();
         }
     };
-    auto step_body = [&](int kt, int stage) {
+    // (direct_c: steps kt + 1 .. kt + SE are full ones)
+    auto step_body = [&](int kt, int stage, auto direct_c) __attribute__((always_inline)) {
         inner(stage);
-        wait_step(min(SE - 2, KT - 2 - kt));
-        if (kt + SE < KT) issue(kt + SE);
+        if constexpr (decltype(direct_c)::value) {
+            wait_step(SE - 2);
+            issue_direct(kt + SE);
+        } else {
+            wait_step(min(SE - 2, KT - 2 - kt));
+            if (kt + SE < KT) issue(kt + SE);
+        }
         // the copies stay ahead of the reads below; the last sub-step's
         // MFMAs interleave with the reads of step kt + 1's first fragments
         __builtin_amdgcn_sched_barrier(0);
@@ -840,11 +846,21 @@ __global__ void __launch_bounds__(WM* WN * 64)
         // SE steps per iteration, so that each stage's LDS base is a
         // constant the fragment reads can take as an immediate offset
         int kt = 0;
-        for (; kt + SE <= KT - 1; kt += SE) {
+        if constexpr (RES) {
+            // the ragged step's code stays out of the unrolled loop: in it,
+            // the block-scaled 256 x 128 tile spilled 560 bytes per lane
+            for (; kt + 2 * SE - 1 < KF; kt += SE) {
 #pragma unroll
-            for (int u = 0; u < SE; ++u) step_body(kt + u, u);
+                for (int u = 0; u < SE; ++u) step_body(kt + u, u, std::true_type{});
+            }
+            for (; kt < KT - 1; ++kt) step_body(kt, kt % SE, std::false_type{});
+        } else {
+            for (; kt + SE <= KT - 1; kt += SE) {
+#pragma unroll
+                for (int u = 0; u < SE; ++u) step_body(kt + u, u, std::false_type{});
+            }
+            for (int u = 0; kt < KT - 1; ++kt, ++u) step_body(kt, u, std::false_type{});
         }
-        for (int u = 0; kt < KT - 1; ++kt, ++u) step_body(kt, u);
     }
     if (KT > 0) {
         inner((KT - 1) % SE);
@@ -1123,6 +1139,7 @@ template <int DIN, int DOUT, int OPB>
 ResFn pick_res_tile(int tile_id) {
     if constexpr (DIN == GE_MXF8_E4M3) {
         if (tile_id == 18) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, true, true, true>;
+        if (tile_id == 19) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 2, false, 64, false, true, true>;
     } else if constexpr (DIN == GE_F8_E4M3) {
         if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, true>;
         if (tile_id == 15) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 128, 4, 2, 4, false, 64, false, false, true>;

@@ -60,7 +60,7 @@ class RmsNorm:
         """The address of a rows x cols matrix with row stride ld."""
         if t is None:
             return None
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise GemmEpilogError(GE_ERR_DTYPE, what)
         if rows > 1 and t.stride(0) != ld:
             raise GemmEpilogError(GE_ERR_SHAPE, what)
