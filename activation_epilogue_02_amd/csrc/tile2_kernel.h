@@ -923,8 +923,8 @@ __global__ void __launch_bounds__(WM* WN * 64)
     }
 
     if constexpr (RES) {
-        res_epilogue<DOUT, C::FM, C::FN, BN, C::NT>(p, mx_all, acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, tn, lane,
-                                                   tid);
+        res_epilogue<DOUT, C::FM, C::FN, BN, C::NT>(p, mx_all, acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, n0, tn, lane,
+                                                   tid, smem);
         return;
     } else {
     // ---- fused epilogue on the accumulators (as in tile_kernel.h) ----

@@ -321,8 +321,8 @@ ge_tile_kernel(KernelArgs p_all, RES... res) {
     }
 
     if constexpr (sizeof...(RES) == 1) {
-        res_epilogue<DOUT, C::FM, C::FN, BN, NT>(p, res..., acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, tn, lane,
-                                                tid);
+        res_epilogue<DOUT, C::FM, C::FN, BN, NT>(p, res..., acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, n0, tn, lane,
+                                                tid, smem);
         return;
     } else {
     // ---- fused epilogue on the accumulators ----

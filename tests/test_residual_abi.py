@@ -62,9 +62,9 @@ def test_plan_kinds():
     ("f16", 65, 128, 8192, GE_OP_T, "tile_id=14 "),
     ("e4m3", 8192, 4096, 64, GE_OP_T, "tile_id=16 "),
     ("e4m3", 4096, 4096, 64, GE_OP_T, "tile_id=15 "),
-    ("e4m3", 2048, 4096, 64, GE_OP_N, "tile_id=8 "),
+    ("e4m3", 1024, 4096, 64, GE_OP_N, "tile_id=8 "),
     ("e4m3", 65, 128, 8192, GE_OP_T, "tile_id=17 "),
-    ("mxf8", 2048, 4096, 4096, GE_OP_T, "tile_id=18 "),
+    ("mxf8", 2048, 4096, 4096, GE_OP_T, "tile_id=19 "),
 ])
 def test_plan_choice(a, m, n, k, op_b, want):
     with handle(m, n, k, a, op_b=op_b) as g:
