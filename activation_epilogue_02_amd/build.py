@@ -27,7 +27,7 @@ SOURCES = ["api.cpp", "tile_launch.hip", "tile_f32.hip", "tile_f16.hip", "tile_b
            "smallm_kernel.hip", "ew_kernel.hip", "norm_api.cpp", "norm_kernel.hip",
            "res_f32_f32.hip", "res_f16_f16.hip", "res_f16_f32.hip", "res_bf16_bf16.hip", "res_bf16_f32.hip",
            "res_f8_bf16.hip", "res_f8_f16.hip", "res_f8_f32.hip", "res_mx_bf16.hip", "res_mx_f16.hip",
-           "res_mx_f32.hip", "res_launch.hip", "skinny_kernel.hip", "grad_kernel.hip"]
+           "res_mx_f32.hip", "res_launch.hip", "pair_f16.hip", "pair_bf16.hip", "skinny_kernel.hip", "grad_kernel.hip"]
 
 COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
           "-Wall", "-Wno-unused-result",

@@ -83,6 +83,8 @@ struct ge_plan_s {
     int64_t ld_dp = 0, ld_t = 0;
     ge_plan_s* g_a = nullptr;
     ge_plan_s* g_b = nullptr;
+    int32_t pair_tile = 0;   // both products in one launch of this tile, or 0
+    size_t bw_t2 = 0;        // weight k x n: dP^T for that launch
 };
 
 namespace {
@@ -923,6 +925,63 @@ int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const vo
 }
 
 // ---- its backward pass ----------------------------------------------------------
+// dA takes a weight k x n as its n x k operand, so the pair, which runs one
+// layout, takes dB = A^T dP with both operands transposed then: dP^T beside A^T.
+static ge_desc pair_desc_b(const ge_plan_s* h) {
+    ge_desc b = h->g_b->d;
+    if (h->d.op_b == GE_OP_N) {
+        b.op_b = GE_OP_T;
+        b.ldb = h->ld_t;
+    }
+    return b;
+}
+
+// The tile that runs both gradients' products in one launch, or 0: not for
+// fp32, nor where a product is small enough for its plan to split its
+// reduction, nor where each fills the chip many times over.  One launch / two
+// (us): 1000 x 520 x 1032 18 / 27, 4096 x 4096 x 4096 (512 tiles of 256 x 256) 249 /
+// 407, 8192 x 4096 x 16384 (3072) 1755 / 1735.
+static int choose_pair_tile(const ge_plan_s* h) {
+    for (const ge_plan_s* g : {h->g_a, h->g_b}) {
+        if (elem_size(g->d.a_type) != 2 || g->path != PATH_TILE) return 0;
+        if (g->tile_id != 6 && g->tile_id != 8 && g->tile_id != 13) return 0;
+        if (g->d.m < 1 || g->d.n < 1 || g->d.k < 1) return 0;
+    }
+    const ge_desc &a = h->g_a->d, b = pair_desc_b(h);
+    const int64_t t256 = ceil_div(a.m, 256) * ceil_div(a.n, 256) + ceil_div(b.m, 256) * ceil_div(b.n, 256);
+    const int64_t t128 = ceil_div(a.m, 128) * ceil_div(a.n, 128) + ceil_div(b.m, 128) * ceil_div(b.n, 128);
+    if (t256 >= 2048) return 0;
+    const int id = t256 >= 256 ? 6 : t128 >= 256 ? 8 : 13;
+    const TileShape* t = find_tile(id);
+    return tile_span_ok(t, a) && tile_span_ok(t, b) ? id : 0;
+}
+
+// One of them: D = A B.
+static KernelArgs pair_args(const ge_desc& d, int tile, const void* A, const void* B, void* D) {
+    const TileShape* t = find_tile(tile);
+    KernelArgs a;
+    memset(&a, 0, sizeof(a));
+    a.A = A;
+    a.B = B;
+    a.D = D;
+    a.m = (int32_t)d.m;
+    a.n = (int32_t)d.n;
+    a.k = (int32_t)d.k;
+    a.epilog = GE_EPILOG_NONE;
+    a.axis = GE_BIAS_COL;
+    a.lda = d.lda;
+    a.ldb = d.ldb;
+    a.ldd = d.ldd;
+    a.tiles_m = (int32_t)ceil_div(d.m, t->bm);
+    a.tiles_n = (int32_t)ceil_div(d.n, t->bn);
+    a.group_m = auto_group_m(t, a.tiles_m, d.a_type);
+    a.split_k = 1;
+    a.k_per_split = a.k;
+    a.k_stagger = auto_k_stagger(t, d.a_type);
+    a.batch = 1;
+    return a;
+}
+
 // dA (m x k) = dP B^T and dB = A^T dP (k x n) or dP^T A (n x k), both on the
 // tile kernels.  Those take A untransposed, so the reduction over the rows of
 // dP needs dP^T (weight n x k) or A^T (weight k x n) laid out once.
@@ -970,6 +1029,8 @@ int gemm_epilog_plan_backward(ge_handle h) {
     delete q.g_b;
     q.g_a = ga;
     q.g_b = gb;
+    q.pair_tile = choose_pair_tile(&q);
+    q.bw_t2 = q.pair_tile && kn ? round_up((size_t)d.n * q.ld_t * es, 256) : 0;
     q.backward = true;
     *h = q;
     return GE_OK;
@@ -978,7 +1039,7 @@ int gemm_epilog_plan_backward(ge_handle h) {
 int gemm_epilog_backward_workspace_size(ge_handle h, size_t* bytes) {
     if (!h || !bytes) return GE_ERR_NULL;
     if (!h->backward) return GE_ERR_STATE;
-    *bytes = h->bw_dp + h->bw_t + h->bw_part + h->bw_gemm;
+    *bytes = h->bw_dp + h->bw_t + h->bw_t2 + h->bw_part + h->bw_gemm;
     return GE_OK;
 }
 
@@ -996,20 +1057,24 @@ int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void*
     if (!aligned(dD, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(aux, 16) || !aligned(dA, 16) ||
         !aligned(dB, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
         return GE_ERR_ALIGN;
-    const size_t need = h->bw_dp + h->bw_t + h->bw_part + h->bw_gemm;
+    const size_t need = h->bw_dp + h->bw_t + h->bw_t2 + h->bw_part + h->bw_gemm;
     if (need > 0 && (!workspace || workspace_bytes < need)) return GE_ERR_WORKSPACE;
     if (test_fail_launch()) return GE_ERR_HIP;
     uint8_t* ws = (uint8_t*)workspace;
-    uint8_t *w_dp = ws, *w_t = ws + h->bw_dp, *w_part = w_t + h->bw_t, *w_gemm = w_part + h->bw_part;
+    uint8_t *w_dp = ws, *w_t = ws + h->bw_dp, *w_t2 = w_t + h->bw_t, *w_part = w_t2 + h->bw_t2,
+            *w_gemm = w_part + h->bw_part;
+    const bool pair = (dA || dB) && h->pair_tile;
+    // dP^T: the weight's gradient for a weight n x k, or for the pair
+    uint8_t* dp_t = !dB ? nullptr : !kn ? w_t : pair ? w_t2 : nullptr;
     const void* dP = act ? w_dp : dD;
     const int64_t len = h->axis == GE_BIAS_COL ? d.n : d.m;
     // a sum over no rows (or columns) is zero; the products write zeros for an empty reduction
-    if (d.m > 0 && d.n > 0 && (act || dbias || (dB && !kn))) {
+    if (d.m > 0 && d.n > 0 && (act || dbias || dp_t)) {
         GradArgs g = {};
         g.src = dD;
         g.aux = aux;
         g.dst = act ? w_dp : nullptr;
-        g.dst_t = dB && !kn ? w_t : nullptr;
+        g.dst_t = dp_t;
         g.partial = dbias ? (float*)w_part : nullptr;
         g.rows = (int32_t)d.m;
         g.cols = (int32_t)d.n;
@@ -1022,16 +1087,8 @@ int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void*
         if (launch_grad_prepare(d.a_type, kind, g, stream) != 0) return GE_ERR_HIP;
     }
     if (dbias && len > 0) {
-        KernelArgs z;
-        memset(&z, 0, sizeof(z));
-        z.bias = dbias;
-        z.partial = (float*)w_part;
-        z.m = (int32_t)d.m;
-        z.n = (int32_t)d.n;
-        z.axis = h->axis;
-        z.batch = 1;
         const int parts = d.m > 0 && d.n > 0 ? (int)ceil_div(h->axis == GE_BIAS_COL ? d.m : d.n, kGradTile) : 0;
-        if (launch_bgrad_reduce(d.a_type, z, parts, stream) != 0) return GE_ERR_HIP;
+        if (launch_grad_bias(d.a_type, (const float*)w_part, parts, (int)len, dbias, stream) != 0) return GE_ERR_HIP;
     }
     if (dB && kn && d.m > 0 && d.k > 0) {
         GradArgs g = {};
@@ -1043,6 +1100,18 @@ int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void*
         g.ld = d.lda;
         g.ldt = h->ld_t;
         if (launch_grad_prepare(d.a_type, GRAD_COPY, g, stream) != 0) return GE_ERR_HIP;
+    }
+    if (pair) {
+        // one gradient alone runs the same kernel, the other without tiles: its
+        // bits do not depend on what else is asked for
+        KernelArgs pa = pair_args(h->g_a->d, h->pair_tile, dP, B, dA);
+        KernelArgs pb = pair_args(pair_desc_b(h), h->pair_tile, w_t, kn ? (const void*)w_t2 : A, dB);
+        if (!dA) pa.tiles_m = 0;
+        if (!dB) pb.tiles_m = 0;
+        // the longer reduction first: its tiles take longest
+        const bool a_first = pa.k >= pb.k;
+        return launch_tile_pair(h->pair_tile, d.a_type, kn ? GE_OP_T : GE_OP_N, a_first ? pa : pb, a_first ? pb : pa,
+                                stream) == 0 ? GE_OK : GE_ERR_HIP;
     }
     int st = GE_OK;
     if (dA)

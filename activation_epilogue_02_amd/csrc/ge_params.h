@@ -91,6 +91,11 @@ struct ResArgs : MxArgs {
     int64_t ldr;
 };
 
+// Second kernel argument of the two-product instantiations.
+struct PairArgs {
+    KernelArgs other;
+};
+
 // Kernel families.
 enum Path : int32_t { PATH_TILE = 1, PATH_SMALLM = 2, PATH_SKINNY = 3 };
 
@@ -167,6 +172,9 @@ int launch_tile_mx(int tile_id, int d_type, int op_b, const KernelArgs& args, co
 // 16 columns of D per workgroup.  mx: block-scaled operands.  Returns a hipError_t.
 int launch_tile_res(int tile_id, int a_type, int d_type, int op_b, const KernelArgs& args, const ResArgs& res,
                     unsigned grid, void* stream);
+// Two plain products of one type and layout of B in one launch (tile 6, 8 or 13);
+// their tile counts and launch orders are in the arguments.
+int launch_tile_pair(int tile_id, int type, int op_b, const KernelArgs& first, const KernelArgs& second, void* stream);
 int launch_skinny(int a_type, int d_type, int mb, int rg, const KernelArgs& args, const ResArgs& res, unsigned grid,
                   void* stream);
 

@@ -21,5 +21,7 @@ enum GradKind { GRAD_COPY = 0, GRAD_PLAIN = 1, GRAD_MASK = 2, GRAD_GELU = 3 };
 constexpr int kGradTile = 64;
 
 int launch_grad_prepare(int type, int kind, const GradArgs& a, void* stream);
+// out[j] = sum over t < parts of partial[t][j], j < len (parts = 0: zeros)
+int launch_grad_bias(int type, const float* partial, int parts, int len, void* out, void* stream);
 
 }  // namespace ge

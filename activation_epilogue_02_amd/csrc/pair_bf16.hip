@@ -1,0 +1,8 @@
+// pair_bf16.hip -- two bf16 products in one launch (the backward pass's).
+#include "tile2_kernel.h"
+
+namespace ge {
+
+PairFn pick_pair_bf16(int op_b, int tile_id) { return pick_pair<GE_BF16>(op_b, tile_id); }
+
+}  // namespace ge

@@ -156,17 +156,32 @@ __device__ __forceinline__ int swz_row(int row) {
     else return lds_swz(row & 31);   // 128-byte rows: eight rows cover the 8 chunk slots
 }
 
+// The second kernel argument.
+template <int EXTRA> struct Tile2Extra { typedef MxArgs T; };
+template <> struct Tile2Extra<1> { typedef ResArgs T; };
+template <> struct Tile2Extra<2> { typedef PairArgs T; };
+
+// This workgroup's product: of a batch, or of a pair.
+template <int EXTRA, typename X>
+__device__ __forceinline__ KernelArgs tile2_product(const KernelArgs& p, const X& extra) {
+    if constexpr (EXTRA == 2) return blockIdx.y ? extra.other : p;
+    else return batch_slice(p, blockIdx.y);
+}
+
 // One kernel template for the plain and the block-scaled (MX) instantiations.
 // Its body stays in the __global__ function itself: moved into a force-inlined
 // device function, the same code compiled to 3x the scalar-register spills
 // and 768 bytes of scratch per lane on the 256 x 256 tile (10x slower).
-// RES: the residual product's instantiations, with the epilogue of
-// res_epilogue.h and its further arguments.
+// EXTRA: the second argument.  1: the residual product's, with the epilogue of
+// res_epilogue.h.  2: a second product of its own shape, taken by the workgroups
+// with blockIdx.y == 1 (both plain, D = A B).
 template <int DIN, int DOUT, int OPB, int BM, int BN, int WM, int WN, int S, bool REG, int RB, bool SPLIT = false,
-          bool MX = false, bool RES = false>
+          bool MX = false, int EXTRA = 0>
 __global__ void __launch_bounds__(WM* WN * 64)
-    ge_tile2_kernel(KernelArgs p_all, typename std::conditional<RES, ResArgs, MxArgs>::type mx_all) {
-    const KernelArgs p = batch_slice(p_all, blockIdx.y);   // this product of a batch
+    ge_tile2_kernel(KernelArgs p_all, typename Tile2Extra<EXTRA>::T mx_all) {
+    const KernelArgs p = tile2_product<EXTRA>(p_all, mx_all);
+    if constexpr (EXTRA == 2)
+        if ((int)blockIdx.x >= p.tiles_m * p.tiles_n) return;
     using C = Tile2Cfg<DIN, DOUT, OPB, BM, BN, WM, WN, S, REG, RB, MX>;
     constexpr int BK = C::BK, SE = C::SE, ESZ = C::ESZ, EPC = C::EPC;
     using Frag = typename std::conditional<ESZ == 1, i32x8, u32x4>::type;
@@ -846,7 +861,7 @@ __global__ void __launch_bounds__(WM* WN * 64)
         // SE steps per iteration, so that each stage's LDS base is a
         // constant the fragment reads can take as an immediate offset
         int kt = 0;
-        if constexpr (RES) {
+        if constexpr (EXTRA != 0) {
             // the ragged step's code stays out of the unrolled loop: in it,
             // the block-scaled 256 x 128 tile spilled 560 bytes per lane
             for (; kt + 2 * SE - 1 < KF; kt += SE) {
@@ -922,10 +937,14 @@ __global__ void __launch_bounds__(WM* WN * 64)
         }
     }
 
-    if constexpr (RES) {
+    if constexpr (EXTRA == 1) {
         res_epilogue<DOUT, C::FM, C::FN, BN, C::NT>(p, mx_all, acc, m0, BM, m0 + wm * C::TM, n0 + wn * C::TN, n0, tn, lane,
                                                    tid, smem);
         return;
+    } else if constexpr (EXTRA == 2) {
+        const ResArgs none = {};
+        res_epilogue_kind<GE_EPILOG_BIAS, DOUT, C::FM, C::FN, BN>(p, none, acc, m0 + wm * C::TM, n0 + wn * C::TN, n0,
+                                                                  lane, tid, C::NT, (float*)smem);
     } else {
     // ---- fused epilogue on the accumulators (as in tile_kernel.h) ----
     // the product's scale: fp8 dequantisation factors, or an alpha for any dtype
@@ -1115,7 +1134,7 @@ __global__ void __launch_bounds__(WM* WN * 64)
             }
         }
     }
-    }   // RES
+    }   // EXTRA
 }
 
 
@@ -1138,17 +1157,17 @@ Tile2Fn pick_op2_mx(int op_b, int tile_id) {
 template <int DIN, int DOUT, int OPB>
 ResFn pick_res_tile(int tile_id) {
     if constexpr (DIN == GE_MXF8_E4M3) {
-        if (tile_id == 18) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, true, true, true>;
-        if (tile_id == 19) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 2, false, 64, false, true, true>;
+        if (tile_id == 18) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, true, true, 1>;
+        if (tile_id == 19) return ge_tile2_kernel<GE_F8_E4M3, DOUT, OPB, 128, 128, 2, 2, 2, false, 64, false, true, 1>;
     } else if constexpr (DIN == GE_F8_E4M3) {
-        if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, true>;
-        if (tile_id == 15) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 128, 4, 2, 4, false, 64, false, false, true>;
-        if (tile_id == 16) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 256, 2, 4, 4, false, 32, false, false, true>;
-        if (tile_id == 17) return ge_tile2_kernel<DIN, DOUT, OPB, 64, 128, 2, 2, 4, false, 64, true, false, true>;
+        if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, 1>;
+        if (tile_id == 15) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 128, 4, 2, 4, false, 64, false, false, 1>;
+        if (tile_id == 16) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 256, 2, 4, 4, false, 32, false, false, 1>;
+        if (tile_id == 17) return ge_tile2_kernel<DIN, DOUT, OPB, 64, 128, 2, 2, 4, false, 64, true, false, 1>;
     } else {
-        if (tile_id == 6) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 256, 2, 4, 4, false, 64, false, false, true>;
-        if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, true>;
-        if (tile_id == 14) return ge_tile2_kernel<DIN, DOUT, OPB, 64, 64, 2, 2, 4, false, 128, true, false, true>;
+        if (tile_id == 6) return ge_tile2_kernel<DIN, DOUT, OPB, 256, 256, 2, 4, 4, false, 64, false, false, 1>;
+        if (tile_id == 8) return ge_tile2_kernel<DIN, DOUT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, 1>;
+        if (tile_id == 14) return ge_tile2_kernel<DIN, DOUT, OPB, 64, 64, 2, 2, 4, false, 128, true, false, 1>;
     }
     return nullptr;
 }
@@ -1156,6 +1175,20 @@ ResFn pick_res_tile(int tile_id) {
 template <int DIN, int DOUT>
 ResFn pick_res_op(int op_b, int tile_id) {
     return op_b == GE_OP_T ? pick_res_tile<DIN, DOUT, GE_OP_T>(tile_id) : pick_res_tile<DIN, DOUT, GE_OP_N>(tile_id);
+}
+
+// Two products in one launch (tiles 6, 8 and 13).
+template <int DT, int OPB>
+PairFn pick_pair_tile(int tile_id) {
+    if (tile_id == 6) return ge_tile2_kernel<DT, DT, OPB, 256, 256, 2, 4, 4, false, 64, false, false, 2>;
+    if (tile_id == 8) return ge_tile2_kernel<DT, DT, OPB, 128, 128, 2, 2, 4, false, 64, false, false, 2>;
+    if (tile_id == 13) return ge_tile2_kernel<DT, DT, OPB, 64, 64, 2, 2, 4, false, 128, false, false, 2>;
+    return nullptr;
+}
+
+template <int DT>
+PairFn pick_pair(int op_b, int tile_id) {
+    return op_b == GE_OP_T ? pick_pair_tile<DT, GE_OP_T>(tile_id) : pick_pair_tile<DT, GE_OP_N>(tile_id);
 }
 
 template <int DIN, int DOUT, int OPB>

@@ -494,5 +494,9 @@ ResFn pick_res_f8_f32(int op_b, int tile_id);
 ResFn pick_res_mx_bf16(int op_b, int tile_id);
 ResFn pick_res_mx_f16(int op_b, int tile_id);
 ResFn pick_res_mx_f32(int op_b, int tile_id);
+// two products in one launch
+typedef void (*PairFn)(KernelArgs, PairArgs);
+PairFn pick_pair_f16(int op_b, int tile_id);
+PairFn pick_pair_bf16(int op_b, int tile_id);
 
 }  // namespace ge
