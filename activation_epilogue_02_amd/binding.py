@@ -411,6 +411,11 @@ class GemmEpilog:
         ldr = d.ldd
         if residual is not None and residual.dtype != D.dtype:
             raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: residual")
+        for v, count in ((row_scale, rows), (col_scale, d.n)):
+            if v is not None and v.dtype is not torch.float32:
+                raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: row_scale or col_scale")
+            if v is not None and (v.numel() < count or not v.is_contiguous()):
+                raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: row_scale or col_scale")
         if rows > 1:   # (a single row has no stride of its own)
             if A.stride(0) != d.lda or D.stride(0) != d.ldd:
                 raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: A or D")

@@ -130,42 +130,82 @@ const TileShape* find_res_tile(int id) {
     return nullptr;
 }
 
-// The residual product's tile: the largest that gives every CU a tile, and
-// below that the smallest, which splits K.  Measured (bias, residual, bf16
-// output; us):
-//   bf16 256 x 256 / 128 x 128: 4096 x 4096 x 4096 (256 large tiles) 149 / 191,
-//     2048 x 4096 x 4096 (128) 89 / 89, 3000 x 2000 x 700 (96) 29 / 23;
-//   bf16 128 x 128 / 64 x 64: 2048 x 4096 x 4096 (512) 89 / 101, 3000 x 2000 x 700
-//     (384) 23 / 24, 512 x 4096 x 4096 (128) 37 / 33, 1000 x 1000 x 1000 (64) 21 / 10;
-//   E4M3 256 x 128 / 128 x 128 / 64 x 128 split-K: 2048 x 4096 x 4096 (256 of the
-//     first) 41 / 48 / 60, 1024 x 4096 x 4096 (128) 33 / 25 / 33, 500 x 2000 x 2000
-//     25 / 19 / 14; 256 x 256 and 256 x 128 at 8192 x 4096 x 16384: 472 / 470;
-//   block-scaled 128 x 128 with two workgroups per CU / one with four stages and
-//     split-K: 8192 x 8192 x 8192 758 / 875, 1300 x 4096 x 4096 (352) 53 / 60,
-//     1024 x 4096 x 4096 (256) 38 / 34.
+// What a tile of the residual product costs: `fixed` us a round (prologue and
+// epilogue) and us per 128 bytes of K, in a full round of `slots` workgroups
+// and in one at most half full.
+struct TileCost {
+    int32_t id, bm, bn, slots;
+    double fixed, full, half;
+};
+
+// The tile of the least estimated time: tiles come in rounds of as many as the
+// chip holds, so 581 tiles of 64 x 64 take as long as 1024 would, and fewer,
+// larger ones win.  The figures are fits to the measured (bias, residual, 16-bit
+// output; us, estimate in brackets):
+//   bf16 256 x 256: 4096 x 4096 x 4096 135 (138), x 1024 44 (42), 2048 x 4096 x 4096 89 (90);
+//   128 x 128: 2048 x 4096 x 4096 89 (91), 4096 x 4096 x 1024 55 (55), 3000 x 2000 x 700 22 (21),
+//     512 x 4096 x 4096 37 (41);
+//   64 x 64: 512 x 4096 x 4096 33 (33), 5287 x 435 x 6081 91 (84), 1000 x 1000 x 1000 10 (10);
+//   E4M3 256 x 128: 2048 x 4096 x 4096 41 (41), 1024 x 4096 x 4096 33 (33);
+//   128 x 128: 2048 x 4096 x 4096 48 (48), 1024 x 4096 x 4096 24 (24), 5401 x 785 x 12557 131 (120);
+//   64 x 128: 1024 x 4096 x 4096 30 (32), 500 x 2000 x 2000 13 (10), 1401 x 1801 x 428 15 (13).
+int cheapest_tile(const TileCost* t, int n, const ge_desc& d) {
+    const double steps = (double)ceil_div(d.k * elem_size(d.a_type), 128);
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < n; ++i) {
+        const int64_t tiles = ceil_div(d.m, t[i].bm) * ceil_div(d.n, t[i].bn), rest = tiles % t[i].slots;
+        double us = (double)(tiles / t[i].slots) * (t[i].fixed + steps * t[i].full);
+        if (rest > 0) us += t[i].fixed + steps * (2 * rest <= t[i].slots ? t[i].half : t[i].full);
+        if (i == 0 || us < least) {
+            best = t[i].id;
+            least = us;
+        }
+    }
+    return best;
+}
+
+// The residual product's tile.  E4M3 256 x 256 has its say where it gives every
+// CU two tiles (8192 x 4096 x 16384: 437 us, as 256 x 128).  Block-scaled 128 x 128:
+// two workgroups per CU against one with four stages and split-K: 8192 x 8192 x
+// 8192 758 / 875, 1300 x 4096 x 4096 (352 tiles) 53 / 60, 1024 x 4096 x 4096 (256) 38 / 34.
 int choose_res_tile(const ge_desc& d) {
-    const int64_t t256 = ceil_div(d.m, 256) * ceil_div(d.n, 256);
+    static const TileCost k16[] = {{6, 256, 256, 256, 10.0, 2.0, 1.25},
+                                   {8, 128, 128, 512, 6.5, 1.32, 0.54},
+                                   {14, 64, 64, 512, 4.0, 0.45, 0.35}};
+    static const TileCost k8[] = {{15, 256, 128, 256, 8.0, 1.02, 0.78},
+                                  {8, 128, 128, 256, 5.0, 0.6, 0.5},
+                                  {17, 64, 128, 256, 5.0, 0.34, 0.3}};
     const int64_t t128 = ceil_div(d.m, 128) * ceil_div(d.n, 128);
     switch (d.a_type) {
     case GE_F32: return t128 >= 256 ? 2 : 1;
     case GE_MXF8_E4M3: return t128 > 256 ? 19 : 18;
     case GE_F8_E4M3:
-        if (t256 >= 512) return 16;
-        if (ceil_div(d.m, 256) * ceil_div(d.n, 128) >= 256) return 15;
-        return t128 >= 256 ? 8 : 17;
+        return ceil_div(d.m, 256) * ceil_div(d.n, 256) >= 512 ? 16 : cheapest_tile(k8, 3, d);
     }
-    if (t256 >= 256) return 6;
-    return t128 >= 256 ? 8 : 14;
+    return cheapest_tile(k16, 3, d);
 }
 
-// K slices of a split-K tile: the largest power of two that keeps the grid
-// within one workgroup per CU and every slice at 16 or more steps (32 beyond
-// 128 workgroups), at most 8 (16 for at most 4 tiles).
-int res_split(int64_t tiles, int64_t steps) {
-    const int cap = tiles <= 4 ? 16 : 8;
+// K slices of a split-K tile: the power of two of the least estimated time, with
+// the grid within one workgroup per CU.  A slice saves its share of the K steps
+// (`us` each); meeting takes about 4 us, the last slice's reading of every
+// partial, and the partials' share of the memory.  Measured, us at 1 / 2 / 4 / 8 slices: block-scaled 923 x 1265 x 7945 (80 tiles)
+// 60 / 42, 713 x 185 x 3841 (12) 33 / 28 / 23 / 25, 512 x 2048 x 4096 (64) 28 / 25 / 24;
+// E4M3 251 x 141 x 6795 (8) 26 / 22 / 17 / 17 (22 at 14), 255 x 86 x 2315 (4) 11 / 13 / 13 / 15,
+// 1000 x 500 x 4096 (64) 13 / 15 / 15; bf16 400 x 700 x 3000 (77) 19 / 16, 111 x 1941 x
+// 1129 (62) 9 / 11 / 11.
+int res_split(const TileShape* t, int a_type, int64_t tiles, int64_t steps) {
+    const double us = a_type == GE_MXF8_E4M3 ? 0.75 : a_type == GE_F8_E4M3 ? 0.34 : 0.4;
     int split = 1;
-    while (split * 2 <= cap && tiles * split * 2 <= 256 && steps >= split * 2 * (tiles * split * 2 > 128 ? 32 : 16))
-        split *= 2;
+    double least = (double)steps * us;
+    for (int s = 2; s <= 16 && tiles * s <= 256 && steps >= 2 * s; s *= 2) {
+        const double part = 4.0 * t->bm * t->bn;   // bytes; read at 0.055 TB/s by one workgroup, 4 TB/s by all
+        const double v = (double)steps * us / s + 4.0 + s * part / 55e3 + 2.0 * (double)(tiles * s) * part / 4e6;
+        if (v < least) {
+            least = v;
+            split = s;
+        }
+    }
     return split;
 }
 
@@ -825,8 +865,7 @@ int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis) {
         q.grid = (unsigned)(tm * tn);
         if (t->kernel == 5) {
             const int64_t step = elem_size(d.a_type) == 2 ? 64 : 128, steps = ceil_div(d.k, step);
-            int split = res_split(tm * tn, steps);
-            if (split > steps) split = steps > 0 ? (int)steps : 1;
+            const int split = res_split(t, d.a_type, tm * tn, steps);
             q.k_per_split = (int32_t)(ceil_div(steps, split) * step);
             q.split_k = q.k_per_split > 0 ? (int32_t)ceil_div(d.k, q.k_per_split) : 1;
             if (q.split_k < 1) q.split_k = 1;
@@ -1086,8 +1125,8 @@ int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void*
         const int kind = e == GE_EPILOG_RELU_AUX_BIAS ? GRAD_MASK : e == GE_EPILOG_GELU_AUX_BIAS ? GRAD_GELU : GRAD_PLAIN;
         if (launch_grad_prepare(d.a_type, kind, g, stream) != 0) return GE_ERR_HIP;
     }
-    if (dbias && len > 0) {
-        const int parts = d.m > 0 && d.n > 0 ? (int)ceil_div(h->axis == GE_BIAS_COL ? d.m : d.n, kGradTile) : 0;
+    const int parts = d.m > 0 && d.n > 0 ? (int)ceil_div(h->axis == GE_BIAS_COL ? d.m : d.n, kGradTile) : 0;
+    if (dbias && len > 0 && !pair) {
         if (launch_grad_bias(d.a_type, (const float*)w_part, parts, (int)len, dbias, stream) != 0) return GE_ERR_HIP;
     }
     if (dB && kn && d.m > 0 && d.k > 0) {
@@ -1110,8 +1149,9 @@ int gemm_epilog_backward(ge_handle h, const void* dD, const void* A, const void*
         if (!dB) pb.tiles_m = 0;
         // the longer reduction first: its tiles take longest
         const bool a_first = pa.k >= pb.k;
-        return launch_tile_pair(h->pair_tile, d.a_type, kn ? GE_OP_T : GE_OP_N, a_first ? pa : pb, a_first ? pb : pa,
-                                stream) == 0 ? GE_OK : GE_ERR_HIP;
+        PairArgs second = {a_first ? pb : pa, (const float*)w_part, dbias, parts, (int32_t)(dbias ? len : 0)};
+        return launch_tile_pair(h->pair_tile, d.a_type, kn ? GE_OP_T : GE_OP_N, a_first ? pa : pb, second, stream) == 0
+                   ? GE_OK : GE_ERR_HIP;
     }
     int st = GE_OK;
     if (dA)

@@ -91,9 +91,14 @@ struct ResArgs : MxArgs {
     int64_t ldr;
 };
 
-// Second kernel argument of the two-product instantiations.
+// Second kernel argument of the two-product instantiations: the other product,
+// and the sum of `parts` rows of partial sums (bias_sum.h) into out, `len` values
+// (0: none).
 struct PairArgs {
     KernelArgs other;
+    const float* partial;
+    void* out;
+    int32_t parts, len;
 };
 
 // Kernel families.
@@ -172,9 +177,9 @@ int launch_tile_mx(int tile_id, int d_type, int op_b, const KernelArgs& args, co
 // 16 columns of D per workgroup.  mx: block-scaled operands.  Returns a hipError_t.
 int launch_tile_res(int tile_id, int a_type, int d_type, int op_b, const KernelArgs& args, const ResArgs& res,
                     unsigned grid, void* stream);
-// Two plain products of one type and layout of B in one launch (tile 6, 8 or 13);
-// their tile counts and launch orders are in the arguments.
-int launch_tile_pair(int tile_id, int type, int op_b, const KernelArgs& first, const KernelArgs& second, void* stream);
+// Two plain products of one type and layout of B, and the sum beside them, in one
+// launch (tile 6, 8 or 13); their tile counts and launch orders are in the arguments.
+int launch_tile_pair(int tile_id, int type, int op_b, const KernelArgs& first, const PairArgs& second, void* stream);
 int launch_skinny(int a_type, int d_type, int mb, int rg, const KernelArgs& args, const ResArgs& res, unsigned grid,
                   void* stream);
 

@@ -6,7 +6,7 @@
 // sums over the tile's rows (or columns) from the fp32 values, and the
 // rounded tile through LDS for the transposed store, so both orders are
 // written in whole lines.  Bound by memory.
-#include "ge_device.h"
+#include "bias_sum.h"
 #include "grad_params.h"
 
 namespace ge {
@@ -144,28 +144,10 @@ __global__ void __launch_bounds__(256) grad_prepare(GradArgs p) {
     }
 }
 
-// The bias gradient from its partial sums, in a fixed order: a workgroup takes
-// 32 entries, 32 groups of lanes every 32nd partial each, then the groups in
-// order (one lane per entry over all partials: 40 us for 128 partials of 4096
-// entries, as long as writing dP).
 template <int DT>
-__global__ void __launch_bounds__(1024) grad_bias(const float* partial, int parts, int len, void* out) {
-    __shared__ float red[32][33];
-    const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int64_t j = (int64_t)blockIdx.x * 32 + c;
-    float v = 0.0f;
-    if (j < len) {
-#pragma unroll 4
-        for (int t = g; t < parts; t += 32) v += partial[(int64_t)t * len + j];
-    }
-    red[g][c] = v;
-    __syncthreads();
-    if (g == 0 && j < len) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s += red[i][c];
-        store_one<DT>(out, j, s);
-    }
+__global__ void __launch_bounds__(256) grad_bias(const float* partial, int parts, int len, void* out) {
+    __shared__ float red[kSumGroups][kSumCols + 1];
+    sum_partials<DT>(partial, parts, len, out, blockIdx.x, threadIdx.x, red);
 }
 
 template <int DT>
@@ -194,8 +176,8 @@ int launch_grad_bias(int type, const float* partial, int parts, int len, void* o
     void (*fn)(const float*, int, int, void*) = type == GE_F32 ? grad_bias<GE_F32> : type == GE_F16 ? grad_bias<GE_F16>
                                                 : type == GE_BF16 ? grad_bias<GE_BF16> : nullptr;
     if (!fn) return (int)hipErrorInvalidDeviceFunction;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((len - 1) / 32 + 1)), dim3(1024), 0, (hipStream_t)stream, partial, parts, len,
-                       out);
+    hipLaunchKernelGGL(fn, dim3((unsigned)((len - 1) / kSumCols + 1)), dim3(256), 0, (hipStream_t)stream, partial, parts,
+                       len, out);
     return (int)hipGetLastError();
 }
 

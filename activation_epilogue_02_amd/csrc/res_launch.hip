@@ -1,5 +1,6 @@
 // res_launch.hip -- launch tables of the residual product's tiles and of two
 // products in one launch.
+#include "bias_sum.h"
 #include "tile_kernel.h"
 
 namespace ge {
@@ -37,17 +38,17 @@ int launch_tile_res(int tile_id, int a_type, int d_type, int op_b, const KernelA
     return (int)hipGetLastError();
 }
 
-int launch_tile_pair(int tile_id, int type, int op_b, const KernelArgs& first, const KernelArgs& second,
-                     void* stream) {
+int launch_tile_pair(int tile_id, int type, int op_b, const KernelArgs& first, const PairArgs& second, void* stream) {
     const TileShape* t = nullptr;
     for (int i = 0; i < kNumTiles; ++i)
         if (kTiles[i].id == tile_id) t = &kTiles[i];
     const PairFn fn = type == GE_F16 ? pick_pair_f16(op_b, tile_id) : type == GE_BF16 ? pick_pair_bf16(op_b, tile_id) : nullptr;
     if (!t || !fn) return (int)hipErrorInvalidDeviceFunction;
-    const int64_t a = (int64_t)first.tiles_m * first.tiles_n, b = (int64_t)second.tiles_m * second.tiles_n;
-    const PairArgs pair = {second};
-    hipLaunchKernelGGL(fn, dim3((unsigned)(a > b ? a : b), 2), dim3(t->wm * t->wn * 64), 0, (hipStream_t)stream, first,
-                       pair);
+    const int64_t a = (int64_t)first.tiles_m * first.tiles_n, b = (int64_t)second.other.tiles_m * second.other.tiles_n;
+    const int64_t c = second.len > 0 ? (second.len - 1) / kSumCols + 1 : 0;
+    const int64_t x = a > b ? (a > c ? a : c) : (b > c ? b : c);
+    hipLaunchKernelGGL(fn, dim3((unsigned)x, c > 0 ? 3 : 2), dim3(t->wm * t->wn * 64), 0, (hipStream_t)stream, first,
+                       second);
     return (int)hipGetLastError();
 }
 

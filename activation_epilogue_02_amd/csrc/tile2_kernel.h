@@ -46,6 +46,7 @@
 #pragma once
 #include <type_traits>
 
+#include "bias_sum.h"
 #include "tile_kernel.h"
 
 namespace ge {
@@ -164,7 +165,7 @@ template <> struct Tile2Extra<2> { typedef PairArgs T; };
 // This workgroup's product: of a batch, or of a pair.
 template <int EXTRA, typename X>
 __device__ __forceinline__ KernelArgs tile2_product(const KernelArgs& p, const X& extra) {
-    if constexpr (EXTRA == 2) return blockIdx.y ? extra.other : p;
+    if constexpr (EXTRA == 2) return blockIdx.y == 1 ? extra.other : p;
     else return batch_slice(p, blockIdx.y);
 }
 
@@ -174,14 +175,21 @@ __device__ __forceinline__ KernelArgs tile2_product(const KernelArgs& p, const X
 // and 768 bytes of scratch per lane on the 256 x 256 tile (10x slower).
 // EXTRA: the second argument.  1: the residual product's, with the epilogue of
 // res_epilogue.h.  2: a second product of its own shape, taken by the workgroups
-// with blockIdx.y == 1 (both plain, D = A B).
+// with blockIdx.y == 1 (both plain, D = A B), and a sum of partials, taken by
+// those with blockIdx.y == 2.
 template <int DIN, int DOUT, int OPB, int BM, int BN, int WM, int WN, int S, bool REG, int RB, bool SPLIT = false,
           bool MX = false, int EXTRA = 0>
 __global__ void __launch_bounds__(WM* WN * 64)
     ge_tile2_kernel(KernelArgs p_all, typename Tile2Extra<EXTRA>::T mx_all) {
     const KernelArgs p = tile2_product<EXTRA>(p_all, mx_all);
-    if constexpr (EXTRA == 2)
+    if constexpr (EXTRA == 2) {
+        if (blockIdx.y == 2) {
+            __shared__ float red[kSumGroups][kSumCols + 1];
+            sum_partials<DOUT>(mx_all.partial, mx_all.parts, mx_all.len, mx_all.out, blockIdx.x, threadIdx.x, red);
+            return;
+        }
         if ((int)blockIdx.x >= p.tiles_m * p.tiles_n) return;
+    }
     using C = Tile2Cfg<DIN, DOUT, OPB, BM, BN, WM, WN, S, REG, RB, MX>;
     constexpr int BK = C::BK, SE = C::SE, ESZ = C::ESZ, EPC = C::EPC;
     using Frag = typename std::conditional<ESZ == 1, i32x8, u32x4>::type;

@@ -43,6 +43,7 @@ class RmsNorm:
         self.rows, self.cols, self.ld, self.ldy = rows, cols, self.desc.ld, self.desc.ldy
         self.dtype = TORCH_DTYPE[t]
         self.out_dtype = self.dtype if o == GE_NORM_PLAIN else torch.float8_e4m3fn
+        self.scale_dtype, self.scale_ld = ((torch.uint8, mx_scale_ld(cols)) if o == GE_NORM_MX else (torch.float32, 1))
         s = ctypes.c_size_t()
         _check(self._lib.ge_rms_norm_workspace_size(self.h, ctypes.byref(s)), "ge_rms_norm_workspace_size")
         self.workspace_bytes = s.value
@@ -57,12 +58,22 @@ class RmsNorm:
         return y, None
 
     def _matrix(self, t, ld, dtype, rows, what) -> Optional[int]:
-        """The address of a rows x cols matrix with row stride ld."""
+        """The address of a matrix of at least `rows` rows of cols values, row stride ld."""
         if t is None:
             return None
         if t.dtype is not dtype:
             raise GemmEpilogError(GE_ERR_DTYPE, what)
-        if rows > 1 and t.stride(0) != ld:
+        if t.numel() < rows * self.cols or (rows > 1 and t.stride(0) != ld):
+            raise GemmEpilogError(GE_ERR_SHAPE, what)
+        return t.data_ptr()
+
+    def _vector(self, t, dtype, count, what) -> Optional[int]:
+        """The address of `count` packed values."""
+        if t is None:
+            return None
+        if t.dtype is not dtype:
+            raise GemmEpilogError(GE_ERR_DTYPE, what)
+        if t.numel() < count or not t.is_contiguous():
             raise GemmEpilogError(GE_ERR_SHAPE, what)
         return t.data_ptr()
 
@@ -72,11 +83,11 @@ class RmsNorm:
         _check(self._lib.ge_rms_norm_forward(
             self.h, n, self._matrix(x, self.ld, self.dtype, n, "RmsNorm.forward: x"),
             self._matrix(residual, self.ld, self.dtype, n, "RmsNorm.forward: residual"),
-            self._matrix(gamma, 1, self.dtype, self.cols, "RmsNorm.forward: gamma"),
+            self._vector(gamma, self.dtype, self.cols, "RmsNorm.forward: gamma"),
             self._matrix(h, self.ld, self.dtype, n, "RmsNorm.forward: h"),
             self._matrix(y, self.ldy, self.out_dtype, n, "RmsNorm.forward: y"),
-            None if scales is None else scales.data_ptr(), None if rstd is None else rstd.data_ptr(),
-            _stream(stream)), "ge_rms_norm_forward")
+            self._vector(scales, self.scale_dtype, n * self.scale_ld, "RmsNorm.forward: scales"),
+            self._vector(rstd, torch.float32, n, "RmsNorm.forward: rstd"), _stream(stream)), "ge_rms_norm_forward")
 
     def backward(self, dy, h, gamma, rstd, dx, dgamma=None, dh=None, workspace=None, rows=None, stream=None):
         """Writes dx (the gradient of x and of the residual) and, if given,
@@ -85,11 +96,11 @@ class RmsNorm:
         _check(self._lib.ge_rms_norm_backward(
             self.h, n, self._matrix(dy, self.ld, self.dtype, n, "RmsNorm.backward: dy"),
             self._matrix(h, self.ld, self.dtype, n, "RmsNorm.backward: h"),
-            self._matrix(gamma, 1, self.dtype, self.cols, "RmsNorm.backward: gamma"),
-            None if rstd is None else rstd.data_ptr(),
+            self._vector(gamma, self.dtype, self.cols, "RmsNorm.backward: gamma"),
+            self._vector(rstd, torch.float32, n, "RmsNorm.backward: rstd"),
             self._matrix(dh, self.ld, self.dtype, n, "RmsNorm.backward: dh"),
             self._matrix(dx, self.ld, self.dtype, n, "RmsNorm.backward: dx"),
-            self._matrix(dgamma, 1, self.dtype, self.cols, "RmsNorm.backward: dgamma"),
+            self._vector(dgamma, self.dtype, self.cols, "RmsNorm.backward: dgamma"),
             None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
             "ge_rms_norm_backward")

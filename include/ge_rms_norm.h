@@ -30,8 +30,9 @@ extern "C" {
 /* Output kinds.
  *   PLAIN     y in x's type
  *   E4M3_ROW  y as E4M3 codes of y_j / s with one fp32 scale per row,
- *             s = max_j |y_j| / 448 (1 when that maximum is 0): the A operand
- *             and row_scale of an E4M3 product (gemm_epilog_execute_residual)
+ *             s = max_j |y_j| / 448, at least 2^-126 (1 when that maximum is 0):
+ *             the A operand and row_scale of an E4M3 product
+ *             (gemm_epilog_execute_residual)
  *   MX        y as E4M3 codes with one E8M0 scale byte per 32 columns: with
  *             a = max |y_j| of the block, byte = floor(log2 a) - 8 + 127
  *             (clamped to 0..254; 127 when a is 0 or not finite): the

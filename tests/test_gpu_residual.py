@@ -188,7 +188,7 @@ def test_long_k(a, d, m, n, k):
 @pytest.mark.parametrize("a,d,m,n,k,tile", [
     ("bf16", "bf16", 4100, 8200, 200, 6), ("f16", "f16", 4100, 8200, 72, 6), ("f16", "f32", 2050, 2100, 264, 8),
     ("bf16", "bf16", 2050, 2100, 264, 8), ("e4m3", "bf16", 4100, 8200, 400, 16), ("e4m3", "f16", 4100, 4100, 1040, 15),
-    ("e4m3", "f32", 2050, 2100, 272, 8), ("mxf8", "bf16", 2050, 2100, 400, 19), ("mxf8", "f16", 700, 2100, 1100, 18),
+    ("e4m3", "f32", 1050, 2100, 272, 8), ("mxf8", "bf16", 2050, 2100, 400, 19), ("mxf8", "f16", 700, 2100, 1100, 18),
     ("f32", "f32", 2050, 2100, 136, 2)])
 @pytest.mark.parametrize("op_b", [GE_OP_N, GE_OP_T], ids=["kn", "nk"])
 def test_large_tiles(a, d, m, n, k, tile, op_b):

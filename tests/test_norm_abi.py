@@ -152,3 +152,23 @@ def test_wrapper_refuses_other_types_and_strides():
         with pytest.raises(B.GemmEpilogError) as e:
             n.forward(torch.zeros(4, 72, dtype=torch.bfloat16)[:, :64], ok[0], ok)
         assert e.value.status == B.GE_ERR_SHAPE
+
+
+def test_wrapper_refuses_short_and_wrong_vectors():
+    import torch
+    ok = torch.zeros(4, 64, dtype=torch.bfloat16)
+    codes = torch.zeros(4, 64, dtype=torch.float8_e4m3fn)
+    scales, gamma = torch.zeros(4), ok[0]
+    with RmsNorm(4, 64, "bf16", out="e4m3_row", ld=64) as n:
+        for bad, status in ((dict(scales=scales.double()), B.GE_ERR_DTYPE), (dict(scales=scales[:3]), B.GE_ERR_SHAPE),
+                            (dict(rstd=scales.half()), B.GE_ERR_DTYPE), (dict(rstd=scales[::2]), B.GE_ERR_SHAPE),
+                            (dict(gamma=gamma[:63]), B.GE_ERR_SHAPE), (dict(x=ok[:3]), B.GE_ERR_SHAPE),
+                            (dict(residual=ok[:1]), B.GE_ERR_SHAPE), (dict(y=codes[:2]), B.GE_ERR_SHAPE)):
+            kw = dict(x=ok, gamma=gamma, y=codes, scales=scales) | bad
+            with pytest.raises(B.GemmEpilogError) as e:
+                n.forward(**kw)
+            assert e.value.status == status, bad
+    with RmsNorm(4, 64, "bf16", out="mx", ld=64) as n:
+        with pytest.raises(B.GemmEpilogError) as e:
+            n.forward(ok, gamma, codes, scales=scales)
+        assert e.value.status == B.GE_ERR_DTYPE
