@@ -25,6 +25,8 @@
 //    same few memory channels.
 //  * The epilogue's operands (bias, scales, residual) are fetched before
 //    the K loop, so that their latency hides under it.
+#include <type_traits>
+
 #include "ge_device.h"
 
 namespace ge {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kWaves * 64) ge_skinny_kernel(KernelArgs p, Re
         for (int b = 0; b < MB; ++b) acc[g][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // spans in flight: what 256 registers per lane hold beside the rest
-    constexpr int U = MX ? (TILES <= 2 ? 4 : TILES <= 4 ? 2 : 1) : TILES <= 2 ? 8 : TILES <= 3 ? 6 : TILES <= 5 ? 4 : 2;
+    constexpr int U = MX ? (TILES <= 2 ? 4 : TILES <= 4 ? 2 : 1) : TILES <= 2 ? 8 : TILES <= 3 ? 6 : TILES <= 4 ? 4 : TILES <= 5 ? 3 : 2;
     struct Slot {
         u32x4 v[TILES][2];
         uint32_t sc[TILES];
@@ -201,29 +203,36 @@ __global__ void __launch_bounds__(kWaves * 64) ge_skinny_kernel(KernelArgs p, Re
             for (int b = 0; b < MB; ++b)
                 acc[g][b] = span_mfma<DIN>(f[g][0], f[g][1], f[RG + b][0], f[RG + b][1], w[g], w[RG + b], acc[g][b]);
     };
-    if (count > 0) {
-        Slot t[U];
-        if (count >= U) {
+    // fewer spans than `most`: the missing ones are read as the last (a branch
+    // around a load would make every wait one for all loads), and not used
+    Slot t[U];
+    auto few = [&](auto most) __attribute__((always_inline)) {
+        constexpr int L = decltype(most)::value;
 #pragma unroll
-            for (int u = 0; u < U; ++u) load(t[u], u);
-        } else {
+        for (int u = 0; u < L; ++u) load(t[u], min(u, count - 1));
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (u < count) load(t[u], u);
-        }
+        for (int u = 0; u < L; ++u)
+            if (u < count) take(t[u], 0, false);
+    };
+    if (count >= U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(t[u], u);
         int i = 0;
         for (; i + 2 * U <= count; i += U) {
 #pragma unroll
             for (int u = 0; u < U; ++u) take(t[u], i + U + u, true);
         }
-        // fewer than 2 U are left
+        // at least U and fewer than 2 U are left
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u < count) take(t[u], i + U + u, i + U + u < count);
+        for (int u = 0; u < U; ++u) take(t[u], i + U + u, i + U + u < count);
         i += U;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + u < count) take(t[u], 0, false);
+    } else if (2 * count > U) {
+        few(std::integral_constant<int, U>{});
+    } else if (count > 0) {
+        few(std::integral_constant<int, (U + 1) / 2>{});
     }
     if (full >= s_begin && full < s_end) {
         // the ragged last span: what lies beyond k is zero in both operands
