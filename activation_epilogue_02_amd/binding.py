@@ -350,7 +350,8 @@ class GemmEpilog:
     """
 
     def __init__(self, m, n, k, a_dtype, d_dtype, op_b=GE_OP_N, lda=None, ldb=None, ldd=None, batch=0):
-        self.desc = make_desc(m, n, k, a_dtype, d_dtype, op_b, lda, ldb, ldd, batch=batch)
+        d = self.desc = make_desc(m, n, k, a_dtype, d_dtype, op_b, lda, ldb, ldd, batch=batch)
+        self._sizes = (d.m, d.n, d.lda, d.ldd)   # (a structure's field takes 0.1 us to read)
         self.h = gemm_epilog_create(self.desc)
         self.epilog = None
 
@@ -406,18 +407,18 @@ class GemmEpilog:
             D, aux_new, ws_new = self.alloc_outputs(A.device)
             aux = aux if aux is not None else aux_new
             workspace = workspace if workspace is not None else ws_new
-        d = self.desc
-        rows = d.m if m is None else m
-        ldr = d.ldd
+        rows, cols, lda, ldr = self._sizes
+        if m is not None:
+            rows = m
         if residual is not None and residual.dtype != D.dtype:
             raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: residual")
-        for v, count in ((row_scale, rows), (col_scale, d.n)):
+        for v, count in ((row_scale, rows), (col_scale, cols)):
             if v is not None and v.dtype is not torch.float32:
                 raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: row_scale or col_scale")
             if v is not None and (v.numel() < count or not v.is_contiguous()):
                 raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: row_scale or col_scale")
         if rows > 1:   # (a single row has no stride of its own)
-            if A.stride(0) != d.lda or D.stride(0) != d.ldd:
+            if A.stride(0) != lda or D.stride(0) != ldr:
                 raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: A or D")
             if residual is not None:
                 ldr = residual.stride(0)

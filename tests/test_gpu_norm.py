@@ -312,3 +312,29 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, h, dx, dg), want)), k
     n.free()
+
+
+def test_more_rows_than_workgroups():
+    """4 M short rows: the launch is bounded and its waves walk the rows."""
+    rows, cols = (1 << 22) + 3, 8
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(rows, cols, generator=g, device="cuda").bfloat16()
+    gamma = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(x, 9.0)
+    with RmsNorm(rows, cols, "bf16", eps=EPS) as n:
+        n.forward(x, gamma, y)
+    near(y, exact(x, None, gamma)[2], torch.bfloat16, K(cols))
+
+
+def test_tiny_rows_keep_a_normal_scale():
+    """A row of values so small that max / 448 is no normal number: its scale is 2^-126, no code is NaN."""
+    x = torch.full((2, 40), 1e-42, device="cuda")
+    x[0, 3] = 0
+    x[1] = 3e-37
+    gamma = torch.ones(40, device="cuda")
+    with RmsNorm(2, 40, "f32", out="e4m3_row", eps=1.0, ld=40) as n:
+        y, s = n.alloc_outputs()
+        n.forward(x, gamma, y, scales=s)
+    assert (s == 2.0 ** -126).all() and (y[0].float() == 0).all()
+    # 3e-37 * 2^126 = 25.5: the nearest code is 26
+    assert (y[1].float() == 26).all()
