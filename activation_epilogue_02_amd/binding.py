@@ -151,6 +151,71 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
+# ---- checks of the tensors a call is given -------------------------------------------
+# The kernels see addresses, sizes and row strides only, so a tensor that does not hold what the plan says would be
+# read or written out of place.  Each helper returns the address.  (Host time of a small call: an attribute of a
+# tensor takes about 0.1 us, so each is read once, and absent tensors cost no call.)
+def _matrix(t, rows, cols, ld, dtype, device, what) -> int:
+    """A matrix of at least rows x cols values with row stride ld (8-bit codes may come as bytes)."""
+    if t.dtype is not dtype and not (t.dtype is torch.uint8 and dtype is torch.float8_e4m3fn):
+        raise GemmEpilogError(GE_ERR_DTYPE, what)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        fits = (stride == (ld, 1) or (rows == 1 or stride[0] == ld) and (cols == 1 or stride[1] == 1)) and (
+            shape[0] >= rows and shape[1] >= cols)
+    else:
+        fits = _holds_rows(t, rows, cols, ld)
+    if not fits and rows > 0 and cols > 0:
+        raise GemmEpilogError(GE_ERR_SHAPE, what)
+    if t.get_device() != device:
+        raise GemmEpilogError(GE_ERR_HIP, what + " is on another device")
+    return t.data_ptr()
+
+
+def _holds_rows(t, rows, cols, ld) -> bool:
+    """The same for a tensor of another rank: rows along the first dimension, or packed storage."""
+    if t.dim() > 1 and t.shape[0] >= rows and (rows == 1 or t.stride(0) == ld):
+        row = t[:1]
+        return row.is_contiguous() and row.numel() >= cols
+    return (t.is_contiguous() and (rows == 1 or t.dim() < 2 or ld in t.stride())
+            and t.numel() >= (rows - 1) * ld + cols)
+
+
+def _vector(t, count, dtype, device, what) -> int:
+    """At least `count` packed values."""
+    if t.dtype is not dtype:
+        raise GemmEpilogError(GE_ERR_DTYPE, what)
+    if t.numel() < count or not t.is_contiguous():
+        raise GemmEpilogError(GE_ERR_SHAPE, what)
+    if t.get_device() != device:
+        raise GemmEpilogError(GE_ERR_HIP, what + " is on another device")
+    return t.data_ptr()
+
+
+def _scale_rows(t, rows, ld, device, what) -> int:
+    """Block scales: rows of ld bytes, packed."""
+    if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e8m0fnu:
+        raise GemmEpilogError(GE_ERR_DTYPE, what)
+    return _vector(t, rows * ld, t.dtype, device, what)
+
+
+def _workspace(t, device, what):
+    """(address, bytes) of a packed tensor of any type."""
+    if not t.is_contiguous():
+        raise GemmEpilogError(GE_ERR_SHAPE, what)
+    if t.get_device() != device:
+        raise GemmEpilogError(GE_ERR_HIP, what + " is on another device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _device(t, what) -> int:
+    """The GPU of a call's output; the call's other tensors have to share it."""
+    d = t.get_device()
+    if d < 0 and torch.cuda.is_available():   # (without a GPU the launch itself reports that)
+        raise GemmEpilogError(GE_ERR_HIP, what + " is not on a GPU")
+    return d
+
+
 def make_desc(m, n, k, a_type, d_type, op_b=GE_OP_N, lda=None, ldb=None, ldd=None,
               b_type=None, bias_type=None, batch=0) -> ge_desc:
     a = DTYPE_CODE[a_type] if not isinstance(a_type, int) else a_type
@@ -351,9 +416,13 @@ class GemmEpilog:
 
     def __init__(self, m, n, k, a_dtype, d_dtype, op_b=GE_OP_N, lda=None, ldb=None, ldd=None, batch=0):
         d = self.desc = make_desc(m, n, k, a_dtype, d_dtype, op_b, lda, ldb, ldd, batch=batch)
-        self._sizes = (d.m, d.n, d.lda, d.ldd)   # (a structure's field takes 0.1 us to read)
         self.h = gemm_epilog_create(self.desc)
-        self.epilog = None
+        self._lib = lib()
+        # (a structure's field takes 0.1 us to read)
+        self._sizes = (d.m, d.n, d.k, d.lda, d.ldd)
+        self._types = (TORCH_DTYPE[d.a_type], TORCH_DTYPE[d.d_type])
+        self._weight = (d.n, d.k, d.ldb) if d.op_b == GE_OP_T else (d.k, d.n, d.ldb)
+        self.epilog = self.axis = None
 
     def plan(self, epilog="bias", axis="row", path=0, unfused=0, tile=0, split_k=0, group_m=0):
         gemm_epilog_plan(self.h, epilog, axis, ge_pref(path, unfused, tile, split_k, group_m))
@@ -395,35 +464,65 @@ class GemmEpilog:
         """Plan for execute_residual: D = residual + act(P), P = s * row_scale[i] * col_scale[j] * A*B + bias."""
         gemm_epilog_plan_residual(self.h, epilog, axis)
         self.epilog = EPILOG_CODE[epilog] if isinstance(epilog, str) else epilog
+        self.axis = AXIS_CODE[axis] if isinstance(axis, str) else axis
         self.ws_bytes = gemm_epilog_workspace_size(self.h)
         self.aux_ld_bits = gemm_epilog_aux_ld(self.h)
         return self
 
+    def _aux(self, aux, rows, device, what) -> int:
+        """aux of `rows` rows as the epilogue lays it out: mask words, or the pre-activation in D's type."""
+        if self.epilog == GE_EPILOG_RELU_AUX_BIAS:
+            return _matrix(aux, rows, self.aux_ld_bits // 32, self.aux_ld_bits // 32, torch.int32, device, what)
+        if self.epilog == GE_EPILOG_GELU_AUX_BIAS:
+            d = self._types[1]
+            return _matrix(aux, rows, self._sizes[1], self.aux_ld_bits // torch.finfo(d).bits, d, device, what)
+        return aux.data_ptr()   # (this epilogue has none: refused)
+
     def execute_residual(self, A, B, bias=None, residual=None, D=None, aux=None, row_scale=None, col_scale=None,
                          a_scales=None, b_scales=None, scale_a=None, scale_b=None, workspace=None, m=None,
                          stream=None):
-        """residual is an m x n matrix in D's dtype (any 16-byte row stride), or None; m: rows of this call."""
+        """residual is an m x n matrix in D's dtype (any 16-byte row stride), or None; m: rows of this call.
+
+        Every tensor has to hold what the call reads or writes, in the planned types and row strides:
+        GemmEpilogError with GE_ERR_DTYPE or GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on D's GPU)."""
         if D is None:
             D, aux_new, ws_new = self.alloc_outputs(A.device)
             aux = aux if aux is not None else aux_new
             workspace = workspace if workspace is not None else ws_new
-        rows, cols, lda, ldr = self._sizes
+        rows, n, k, lda, ldr = self._sizes
         if m is not None:
             rows = m
-        if residual is not None and residual.dtype != D.dtype:
-            raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: residual")
-        for v, count in ((row_scale, rows), (col_scale, cols)):
-            if v is not None and v.dtype is not torch.float32:
-                raise GemmEpilogError(GE_ERR_DTYPE, "execute_residual: row_scale or col_scale")
-            if v is not None and (v.numel() < count or not v.is_contiguous()):
-                raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: row_scale or col_scale")
-        if rows > 1:   # (a single row has no stride of its own)
-            if A.stride(0) != lda or D.stride(0) != ldr:
-                raise GemmEpilogError(GE_ERR_SHAPE, "execute_residual: A or D")
-            if residual is not None:
+        a_type, d_type = self._types
+        dev = _device(D, "execute_residual: D")
+        d = _matrix(D, rows, n, ldr, d_type, dev, "execute_residual: D")
+        a = None if A is None else _matrix(A, rows, k, lda, a_type, dev, "execute_residual: A")
+        b = None if B is None else _matrix(B, *self._weight, a_type, dev, "execute_residual: B")
+        r = bv = rs = cs = sa = sb = fa = fb = ax = ws = None
+        ws_bytes, f32 = 0, torch.float32
+        if residual is not None:
+            if rows > 1:   # (a single row has no stride of its own)
                 ldr = residual.stride(0)
-        gemm_epilog_execute_residual(self.h, rows, A, B, bias, residual, ldr, D, aux, row_scale, col_scale, a_scales,
-                                     b_scales, scale_a, scale_b, workspace, None, stream)
+            r = _matrix(residual, rows, n, ldr, d_type, dev, "execute_residual: residual")
+        if bias is not None:
+            bv = _vector(bias, rows if self.axis == GE_BIAS_ROW else n, d_type, dev, "execute_residual: bias")
+        if row_scale is not None:
+            rs = _vector(row_scale, rows, f32, dev, "execute_residual: row_scale")
+        if col_scale is not None:
+            cs = _vector(col_scale, n, f32, dev, "execute_residual: col_scale")
+        if a_scales is not None:
+            sa = _scale_rows(a_scales, rows, mx_scale_ld(k), dev, "execute_residual: a_scales")
+        if b_scales is not None:
+            sb = _scale_rows(b_scales, n, mx_scale_ld(k), dev, "execute_residual: b_scales")
+        if scale_a is not None:
+            fa = _vector(scale_a, 1, f32, dev, "execute_residual: scale_a")
+        if scale_b is not None:
+            fb = _vector(scale_b, 1, f32, dev, "execute_residual: scale_b")
+        if aux is not None:
+            ax = self._aux(aux, rows, dev, "execute_residual: aux")
+        if workspace is not None:
+            ws, ws_bytes = _workspace(workspace, dev, "execute_residual: workspace")
+        _check(self._lib.gemm_epilog_execute_residual(self.h, rows, a, b, sa, sb, bv, r, ldr, rs, cs, fa, fb, d, ax, ws,
+                                                      ws_bytes, _stream(stream)), "gemm_epilog_execute_residual")
         return D, aux
 
     def plan_backward(self):

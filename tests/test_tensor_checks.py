@@ -1,0 +1,139 @@
+"""What the tensor-level calls refuse before they reach the library: tensors that do not hold what the plan reads or
+writes.  Nothing is launched: a call that passes every check reports GE_ERR_HIP here."""
+import pytest
+import torch
+
+from activation_epilogue_02_amd import GE_OP_N, GE_OP_T, GemmEpilog, mx_scale_ld
+from activation_epilogue_02_amd import binding as B
+
+BF, E4 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(autouse=True)
+def no_launch(monkeypatch):
+    monkeypatch.setenv("GE_TEST_FAIL_LAUNCH", "1")
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)   # (tensors here are on the CPU)
+
+
+def status(f, *a, **kw):
+    with pytest.raises(B.GemmEpilogError) as e:
+        f(*a, **kw)
+    return e.value.status
+
+
+def room(rows, cols, dtype=BF, pad=8):
+    """rows x cols with a row stride of cols + pad."""
+    return torch.zeros(rows, cols + pad, dtype=torch.uint8 if dtype is E4 else dtype).view(dtype)[:, :cols]
+
+
+OK, SHAPE, DTYPE = B.GE_ERR_HIP, B.GE_ERR_SHAPE, B.GE_ERR_DTYPE
+
+
+def residual_args(m=100, n=64, k=128):
+    return dict(A=room(m, k), B=room(n, k), bias=torch.zeros(n, dtype=BF), residual=room(m, n, pad=16), D=room(m, n),
+                row_scale=torch.zeros(m), col_scale=torch.zeros(n), scale_a=torch.zeros(1),
+                workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("bad,want", [
+    ({}, OK),
+    (dict(A=room(4, 128)), SHAPE),                        # fewer rows than the call
+    (dict(A=room(100, 128)[:, ::2]), SHAPE),
+    (dict(A=room(100, 256)[:, ::2]), SHAPE),
+    (dict(A=torch.empty_like(room(100, 128)).contiguous()), SHAPE),   # packed rows, another stride
+    (dict(A=torch.zeros(1, 136, dtype=BF).expand(100, 136)), SHAPE),
+    (dict(A=room(100, 128, torch.float16)), DTYPE),
+    (dict(A=room(100, 128, torch.float32)), DTYPE),
+    (dict(B=room(63, 128)), SHAPE),
+    (dict(B=room(64, 128, pad=0)), SHAPE),
+    (dict(B=room(136, 56).t()), SHAPE),
+    (dict(B=room(64, 128, torch.float32)), DTYPE),
+    (dict(bias=torch.zeros(4)), DTYPE),
+    (dict(bias=torch.zeros(63, dtype=BF)), SHAPE),
+    (dict(bias=torch.zeros(128, dtype=BF)[::2]), SHAPE),
+    (dict(bias=torch.zeros(1, dtype=BF).expand(64)), SHAPE),
+    (dict(residual=room(99, 64)), SHAPE),
+    (dict(residual=room(100, 56)), SHAPE),
+    (dict(residual=room(100, 64, torch.float16)), DTYPE),
+    (dict(residual=torch.zeros(1, 64, dtype=BF).expand(100, 64)), SHAPE),
+    (dict(residual=torch.zeros(100, 1, dtype=BF).expand(100, 64)), SHAPE),
+    (dict(D=room(99, 64)), SHAPE),
+    (dict(D=room(100, 64, pad=0)), SHAPE),
+    (dict(D=room(100, 64, torch.float32)), DTYPE),
+    (dict(D=room(100, 64, torch.float32), residual=room(100, 64, torch.float32)), DTYPE),
+    (dict(row_scale=torch.zeros(99)), SHAPE),
+    (dict(col_scale=torch.zeros(64, dtype=torch.float64)), DTYPE),
+    (dict(scale_a=torch.zeros(0)), SHAPE),
+    (dict(scale_b=torch.zeros(1, dtype=torch.float64)), DTYPE),
+    (dict(workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 20)), SHAPE),
+    (dict(m=4, A=room(4, 128), residual=room(4, 64), D=room(4, 64)), OK),
+    (dict(m=4, A=room(3, 128)), SHAPE),
+    (dict(m=1, A=torch.zeros(128, dtype=BF), D=torch.zeros(1, 1, 64, dtype=BF)), OK),   # one row of any rank
+    (dict(m=1, A=torch.zeros(127, dtype=BF)), SHAPE),
+    (dict(m=1, A=torch.zeros(1, 1, dtype=BF).expand(1, 128)), SHAPE),
+    (dict(m=1, A=torch.zeros(256, dtype=BF)[::2]), SHAPE),
+    (dict(A=torch.zeros(100, 2, 68, dtype=BF)), OK),                  # a row as heads
+    (dict(A=torch.zeros(100, 2, 64, dtype=BF)), SHAPE),
+    (dict(B=torch.zeros(64 * 136, dtype=BF)), OK),                    # a plain buffer of the layout
+    (dict(B=torch.zeros(64 * 136 - 9, dtype=BF)), SHAPE),
+], ids=lambda v: " ".join(f"{k}:{tuple(t.shape)}/{t.stride()}" if torch.is_tensor(t) else f"{k}:{t}"
+                          for k, t in v.items()) if isinstance(v, dict) else str(v))
+def test_execute_residual(bad, want):
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
+        g.plan_residual("bias")
+        assert status(g.execute_residual, **residual_args() | bad) == want
+
+
+def test_execute_residual_row_bias_and_kn():
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_N, 136, 72, 72) as g:
+        g.plan_residual("bias", "row")
+        a = residual_args() | dict(B=room(128, 64))
+        assert status(g.execute_residual, **a) == SHAPE                       # 64 values for 100 rows
+        a["bias"] = torch.zeros(100, dtype=BF)
+        assert status(g.execute_residual, **a) == OK
+        assert status(g.execute_residual, **a | dict(B=room(64, 128, pad=8))) == SHAPE
+
+
+def test_execute_residual_eight_bits():
+    for kind, extra in (("e4m3", {}), ("mxf8", dict(a_scales=torch.zeros(100, mx_scale_ld(128), dtype=torch.uint8),
+                                                    b_scales=torch.zeros(64, mx_scale_ld(128), dtype=torch.uint8)))):
+        with GemmEpilog(100, 64, 128, kind, "bf16", GE_OP_T, 144, 144, 72) as g:
+            g.plan_residual("bias")
+            a = residual_args() | dict(A=room(100, 128, E4, 16), B=room(64, 128, E4, 16)) | extra
+            assert status(g.execute_residual, **a) == OK
+            assert status(g.execute_residual, **a | dict(A=a["A"].view(torch.uint8))) == OK   # codes as bytes
+            assert status(g.execute_residual, **a | dict(A=room(100, 128, torch.int8, 16))) == DTYPE
+            if extra:
+                assert status(g.execute_residual, **a | dict(a_scales=extra["a_scales"].float())) == DTYPE
+                assert status(g.execute_residual, **a | dict(a_scales=extra["a_scales"][:99])) == SHAPE
+                assert status(g.execute_residual, **a | dict(b_scales=extra["b_scales"][:, :4])) == SHAPE
+                e8 = extra["a_scales"].view(torch.float8_e8m0fnu)
+                assert status(g.execute_residual, **a | dict(a_scales=e8)) == OK
+
+
+def test_execute_residual_aux():
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
+        g.plan_residual("relu_aux_bias")
+        for aux, want in ((torch.zeros(100, 4, dtype=torch.int32), OK), (torch.zeros(99, 4, dtype=torch.int32), SHAPE),
+                          (torch.zeros(100, 2, dtype=torch.int32), SHAPE), (torch.zeros(100, 4), DTYPE)):
+            assert status(g.execute_residual, aux=aux, **residual_args()) == want
+        g.plan_residual("gelu_aux_bias")
+        for aux, want in ((torch.zeros(100, 128, dtype=BF), OK), (torch.zeros(100, 128, dtype=BF)[:, :64], OK),
+                          (torch.zeros(100, 64, dtype=BF), SHAPE), (torch.zeros(100, 128, dtype=torch.float16), DTYPE)):
+            assert status(g.execute_residual, aux=aux, **residual_args()) == want
+        g.plan_residual("bias")
+        assert status(g.execute_residual, aux=aux, **residual_args()) == B.GE_ERR_EPILOG
+
+
+def test_before_a_plan():
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
+        assert status(g.execute_residual, **residual_args()) == B.GE_ERR_STATE
+
+
+def test_tensors_off_the_gpu(monkeypatch):
+    """Where there is a GPU, host memory never reaches a kernel."""
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
+        g.plan_residual("bias")
+        with pytest.raises(B.GemmEpilogError, match="not on a GPU"):
+            g.execute_residual(**residual_args())
