@@ -532,8 +532,25 @@ class GemmEpilog:
         return self
 
     def backward(self, dD, A, B, dA=None, dB=None, dbias=None, aux=None, workspace=None, stream=None):
-        """Writes dA, dB and dbias (those given); dD has D's layout, dA A's and dB B's."""
-        gemm_epilog_backward(self.h, dD, A, B, aux, dA, dB, dbias, workspace, None, stream)
+        """Writes dA, dB and dbias (those given); dD has D's layout, dA A's and dB B's.
+
+        Every tensor is checked against the plan as in execute_residual."""
+        m, n, k, lda, ldd = self._sizes
+        t = self._types[0]
+        first = next((v for v in (dD, A, B, dA, dB, dbias) if v is not None), None)
+        dev = -1 if first is None else _device(first, "backward: dD")
+        dd = None if dD is None else _matrix(dD, m, n, ldd, t, dev, "backward: dD")
+        # (the library refuses the absence of what a wanted gradient reads)
+        a = None if A is None else _matrix(A, m, k, lda, t, dev, "backward: A")
+        b = None if B is None else _matrix(B, *self._weight, t, dev, "backward: B")
+        ga = None if dA is None else _matrix(dA, m, k, lda, t, dev, "backward: dA")
+        gb = None if dB is None else _matrix(dB, *self._weight, t, dev, "backward: dB")
+        gv = (None if dbias is None
+              else _vector(dbias, m if self.axis == GE_BIAS_ROW else n, t, dev, "backward: dbias"))
+        ax = None if aux is None else self._aux(aux, m, dev, "backward: aux")
+        ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace, dev, "backward: workspace")
+        _check(self._lib.gemm_epilog_backward(self.h, dd, a, b, ax, ga, gb, gv, ws, ws_bytes, _stream(stream)),
+               "gemm_epilog_backward")
         return dA, dB, dbias
 
     def describe(self) -> str:

@@ -137,3 +137,59 @@ def test_tensors_off_the_gpu(monkeypatch):
         g.plan_residual("bias")
         with pytest.raises(B.GemmEpilogError, match="not on a GPU"):
             g.execute_residual(**residual_args())
+
+
+def backward_args(m=100, n=64, k=128):
+    return dict(dD=room(m, n), A=room(m, k), B=room(n, k), dA=room(m, k), dB=room(n, k), dbias=torch.zeros(n, dtype=BF),
+                workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("bad,want", [
+    ({}, OK),
+    (dict(dD=torch.ones(1, dtype=BF).expand(100, 64)), SHAPE),        # the gradient of a sum
+    (dict(dD=None), B.GE_ERR_NULL),
+    (dict(dD=room(100, 64, pad=0)), SHAPE),
+    (dict(dD=room(99, 64)), SHAPE),
+    (dict(dD=room(64, 100).t()), SHAPE),
+    (dict(dD=room(100, 64, torch.float32)), DTYPE),
+    (dict(A=room(100, 128, pad=0)), SHAPE),
+    (dict(A=room(100, 128, torch.float16)), DTYPE),
+    (dict(A=None, dB=None), OK),
+    (dict(A=None), B.GE_ERR_NULL),
+    (dict(B=room(64, 128, pad=16)), SHAPE),
+    (dict(B=None, dA=None), OK),
+    (dict(dA=room(4, 128)), SHAPE),
+    (dict(dA=torch.zeros(100, 128, dtype=BF)), SHAPE),                # as empty_like of a padded view gives
+    (dict(dA=room(100, 128, torch.float32)), DTYPE),
+    (dict(dB=torch.zeros(64, 128, dtype=BF)), SHAPE),
+    (dict(dB=room(128, 128)[:, ::2]), SHAPE),
+    (dict(dbias=torch.zeros(63, dtype=BF)), SHAPE),
+    (dict(dbias=torch.zeros(64)), DTYPE),
+    (dict(workspace=None), B.GE_ERR_WORKSPACE),
+    (dict(workspace=torch.zeros(1 << 21, dtype=torch.uint8)[::2]), SHAPE),
+], ids=lambda v: " ".join(f"{k}:{tuple(t.shape)}/{t.stride()}" if torch.is_tensor(t) else f"{k}:{t}"
+                          for k, t in v.items()) if isinstance(v, dict) else str(v))
+def test_backward(bad, want):
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
+        g.plan_residual("bias").plan_backward()
+        assert status(g.backward, **backward_args() | bad) == want
+
+
+def test_backward_aux_and_row_bias():
+    with GemmEpilog(100, 64, 128, "f16", "f16", GE_OP_T, 136, 136, 72) as g:
+        a = {k: v.half() if v.dtype is BF and k == "dbias" else room(*v.shape, torch.float16) if v.dtype is BF else v
+             for k, v in backward_args().items()}
+        g.plan_residual("gelu_aux_bias", "row").plan_backward()
+        aux = torch.zeros(100, 128, dtype=torch.float16)
+        assert status(g.backward, **a, aux=aux) == SHAPE                      # 64 values for 100 rows
+        a["dbias"] = torch.zeros(100, dtype=torch.float16)
+        assert status(g.backward, **a, aux=aux) == OK
+        assert status(g.backward, **a, aux=aux[:99]) == SHAPE
+        assert status(g.backward, **a, aux=aux.bfloat16()) == DTYPE
+        assert status(g.backward, **a, aux=aux[:, :64].contiguous()) == SHAPE
+        assert status(g.backward, **a) == B.GE_ERR_EPILOG
+
+
+def test_backward_before_a_plan():
+    with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
+        assert status(g.backward, **backward_args()) == B.GE_ERR_STATE
