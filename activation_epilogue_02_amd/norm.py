@@ -4,12 +4,11 @@ every step runs in the library's HIP kernels)."""
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
 
 import torch
 
-from .binding import (DTYPE_CODE, ELEM_SIZE, GE_ERR_DTYPE, GE_ERR_SHAPE, TORCH_DTYPE, GemmEpilogError, _check,
-                      _stream, ge_norm_desc, lib, mx_scale_ld)
+from .binding import (DTYPE_CODE, ELEM_SIZE, TORCH_DTYPE, _check, _device, _matrix, _scale_rows, _stream, _vector,
+                      _workspace, ge_norm_desc, lib, mx_scale_ld)
 
 GE_NORM_PLAIN, GE_NORM_E4M3_ROW, GE_NORM_MX = 0, 1, 2
 NORM_OUT_CODE = {"plain": GE_NORM_PLAIN, "e4m3_row": GE_NORM_E4M3_ROW, "mx": GE_NORM_MX}
@@ -57,53 +56,44 @@ class RmsNorm:
             return y, torch.full((self.rows, mx_scale_ld(self.cols)), 127, dtype=torch.uint8, device=device)
         return y, None
 
-    def _matrix(self, t, ld, dtype, rows, what) -> Optional[int]:
-        """The address of a matrix of at least `rows` rows of cols values, row stride ld."""
-        if t is None:
-            return None
-        if t.dtype is not dtype:
-            raise GemmEpilogError(GE_ERR_DTYPE, what)
-        if t.numel() < rows * self.cols or (rows > 1 and t.stride(0) != ld):
-            raise GemmEpilogError(GE_ERR_SHAPE, what)
-        return t.data_ptr()
-
-    def _vector(self, t, dtype, count, what) -> Optional[int]:
-        """The address of `count` packed values."""
-        if t is None:
-            return None
-        if t.dtype is not dtype:
-            raise GemmEpilogError(GE_ERR_DTYPE, what)
-        if t.numel() < count or not t.is_contiguous():
-            raise GemmEpilogError(GE_ERR_SHAPE, what)
-        return t.data_ptr()
-
     def forward(self, x, gamma, y, residual=None, h=None, scales=None, rstd=None, rows=None, stream=None):
-        """Writes y (and scales, h, rstd where given) for `rows` rows."""
-        n = self.rows if rows is None else rows
-        _check(self._lib.ge_rms_norm_forward(
-            self.h, n, self._matrix(x, self.ld, self.dtype, n, "RmsNorm.forward: x"),
-            self._matrix(residual, self.ld, self.dtype, n, "RmsNorm.forward: residual"),
-            self._vector(gamma, self.dtype, self.cols, "RmsNorm.forward: gamma"),
-            self._matrix(h, self.ld, self.dtype, n, "RmsNorm.forward: h"),
-            self._matrix(y, self.ldy, self.out_dtype, n, "RmsNorm.forward: y"),
-            self._vector(scales, self.scale_dtype, n * self.scale_ld, "RmsNorm.forward: scales"),
-            self._vector(rstd, torch.float32, n, "RmsNorm.forward: rstd"), _stream(stream)), "ge_rms_norm_forward")
+        """Writes y (and scales, h, rstd where given) for `rows` rows.
+
+        Every tensor has to hold those rows in the handle's types and strides: GemmEpilogError with GE_ERR_DTYPE or
+        GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on y's GPU)."""
+        n, cols, ld, t = self.rows if rows is None else rows, self.cols, self.ld, self.dtype
+        first = y if y is not None else gamma   # (the library refuses what is missing)
+        dev = -1 if first is None else _device(first, "RmsNorm.forward: y")
+        xp = None if x is None else _matrix(x, n, cols, ld, t, dev, "RmsNorm.forward: x")
+        rp = None if residual is None else _matrix(residual, n, cols, ld, t, dev, "RmsNorm.forward: residual")
+        gp = None if gamma is None else _vector(gamma, cols, t, dev, "RmsNorm.forward: gamma")
+        hp = None if h is None else _matrix(h, n, cols, ld, t, dev, "RmsNorm.forward: h")
+        yp = None if y is None else _matrix(y, n, cols, self.ldy, self.out_dtype, dev, "RmsNorm.forward: y")
+        sp = None
+        if scales is not None:
+            sp = (_scale_rows(scales, n, self.scale_ld, dev, "RmsNorm.forward: scales")
+                  if self.scale_dtype is torch.uint8 else
+                  _vector(scales, n, torch.float32, dev, "RmsNorm.forward: scales"))
+        vp = None if rstd is None else _vector(rstd, n, torch.float32, dev, "RmsNorm.forward: rstd")
+        _check(self._lib.ge_rms_norm_forward(self.h, n, xp, rp, gp, hp, yp, sp, vp, _stream(stream)),
+               "ge_rms_norm_forward")
 
     def backward(self, dy, h, gamma, rstd, dx, dgamma=None, dh=None, workspace=None, rows=None, stream=None):
         """Writes dx (the gradient of x and of the residual) and, if given,
-        dgamma, which needs a workspace of workspace_bytes."""
-        n = self.rows if rows is None else rows
-        _check(self._lib.ge_rms_norm_backward(
-            self.h, n, self._matrix(dy, self.ld, self.dtype, n, "RmsNorm.backward: dy"),
-            self._matrix(h, self.ld, self.dtype, n, "RmsNorm.backward: h"),
-            self._vector(gamma, self.dtype, self.cols, "RmsNorm.backward: gamma"),
-            self._vector(rstd, torch.float32, n, "RmsNorm.backward: rstd"),
-            self._matrix(dh, self.ld, self.dtype, n, "RmsNorm.backward: dh"),
-            self._matrix(dx, self.ld, self.dtype, n, "RmsNorm.backward: dx"),
-            self._vector(dgamma, self.dtype, self.cols, "RmsNorm.backward: dgamma"),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
-            "ge_rms_norm_backward")
+        dgamma, which needs a workspace of workspace_bytes.  Checks as forward's."""
+        n, cols, ld, t = self.rows if rows is None else rows, self.cols, self.ld, self.dtype
+        first = dx if dx is not None else gamma
+        dev = -1 if first is None else _device(first, "RmsNorm.backward: dx")
+        yp = None if dy is None else _matrix(dy, n, cols, ld, t, dev, "RmsNorm.backward: dy")
+        hp = None if h is None else _matrix(h, n, cols, ld, t, dev, "RmsNorm.backward: h")
+        gp = None if gamma is None else _vector(gamma, cols, t, dev, "RmsNorm.backward: gamma")
+        vp = None if rstd is None else _vector(rstd, n, torch.float32, dev, "RmsNorm.backward: rstd")
+        ep = None if dh is None else _matrix(dh, n, cols, ld, t, dev, "RmsNorm.backward: dh")
+        xp = None if dx is None else _matrix(dx, n, cols, ld, t, dev, "RmsNorm.backward: dx")
+        dp = None if dgamma is None else _vector(dgamma, cols, t, dev, "RmsNorm.backward: dgamma")
+        ws, size = (None, 0) if workspace is None else _workspace(workspace, dev, "RmsNorm.backward: workspace")
+        _check(self._lib.ge_rms_norm_backward(self.h, n, yp, hp, gp, vp, ep, xp, dp, ws, size, _stream(stream)),
+               "ge_rms_norm_backward")
 
     def describe(self) -> str:
         buf = ctypes.create_string_buffer(256)

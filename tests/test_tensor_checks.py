@@ -3,7 +3,7 @@ writes.  Nothing is launched: a call that passes every check reports GE_ERR_HIP 
 import pytest
 import torch
 
-from activation_epilogue_02_amd import GE_OP_N, GE_OP_T, GemmEpilog, mx_scale_ld
+from activation_epilogue_02_amd import GE_OP_N, GE_OP_T, GemmEpilog, RmsNorm, mx_scale_ld
 from activation_epilogue_02_amd import binding as B
 
 BF, E4 = torch.bfloat16, torch.float8_e4m3fn
@@ -24,6 +24,11 @@ def status(f, *a, **kw):
 def room(rows, cols, dtype=BF, pad=8):
     """rows x cols with a row stride of cols + pad."""
     return torch.zeros(rows, cols + pad, dtype=torch.uint8 if dtype is E4 else dtype).view(dtype)[:, :cols]
+
+
+def ids(v):
+    return " ".join(f"{k}:{tuple(t.shape)}/{t.stride()}" if torch.is_tensor(t) else f"{k}:{t}"
+                    for k, t in v.items()) if isinstance(v, dict) else str(v)
 
 
 OK, SHAPE, DTYPE = B.GE_ERR_HIP, B.GE_ERR_SHAPE, B.GE_ERR_DTYPE
@@ -76,8 +81,7 @@ def residual_args(m=100, n=64, k=128):
     (dict(A=torch.zeros(100, 2, 64, dtype=BF)), SHAPE),
     (dict(B=torch.zeros(64 * 136, dtype=BF)), OK),                    # a plain buffer of the layout
     (dict(B=torch.zeros(64 * 136 - 9, dtype=BF)), SHAPE),
-], ids=lambda v: " ".join(f"{k}:{tuple(t.shape)}/{t.stride()}" if torch.is_tensor(t) else f"{k}:{t}"
-                          for k, t in v.items()) if isinstance(v, dict) else str(v))
+], ids=ids)
 def test_execute_residual(bad, want):
     with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
         g.plan_residual("bias")
@@ -167,8 +171,7 @@ def backward_args(m=100, n=64, k=128):
     (dict(dbias=torch.zeros(64)), DTYPE),
     (dict(workspace=None), B.GE_ERR_WORKSPACE),
     (dict(workspace=torch.zeros(1 << 21, dtype=torch.uint8)[::2]), SHAPE),
-], ids=lambda v: " ".join(f"{k}:{tuple(t.shape)}/{t.stride()}" if torch.is_tensor(t) else f"{k}:{t}"
-                          for k, t in v.items()) if isinstance(v, dict) else str(v))
+], ids=ids)
 def test_backward(bad, want):
     with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
         g.plan_residual("bias").plan_backward()
@@ -193,3 +196,73 @@ def test_backward_aux_and_row_bias():
 def test_backward_before_a_plan():
     with GemmEpilog(100, 64, 128, "bf16", "bf16", GE_OP_T, 136, 136, 72) as g:
         assert status(g.backward, **backward_args()) == B.GE_ERR_STATE
+
+
+def norm_args(rows=20, cols=64, dtype=BF):
+    return dict(x=room(rows, cols, dtype), gamma=torch.zeros(cols, dtype=dtype), y=room(rows, cols, dtype),
+                residual=room(rows, cols, dtype), h=room(rows, cols, dtype), rstd=torch.zeros(rows))
+
+
+@pytest.mark.parametrize("bad,want", [
+    ({}, OK),
+    (dict(x=room(20, 136)[:, ::2]), SHAPE),                           # every other value
+    (dict(x=torch.zeros(20, 72, dtype=BF)[:, :1].expand(20, 64)), SHAPE),
+    (dict(x=torch.zeros(40, 72, dtype=BF)[:, :32]), SHAPE),           # enough values, short rows
+    (dict(x=room(64, 72, pad=0).t()), SHAPE),
+    (dict(x=room(19, 64)), SHAPE),
+    (dict(x=None), B.GE_ERR_NULL),
+    (dict(gamma=None), B.GE_ERR_NULL),
+    (dict(y=None), B.GE_ERR_NULL),
+    (dict(x=room(20, 64, torch.float16)), DTYPE),
+    (dict(y=room(20, 144)[:, ::2]), SHAPE),
+    (dict(residual=torch.zeros(1, 72, dtype=BF).expand(20, 72)), SHAPE),
+    (dict(h=room(20, 64, pad=0)), SHAPE),
+    (dict(x=torch.zeros(20, 2, 36, dtype=BF)), OK),                   # a row as heads
+    (dict(x=torch.zeros(20, 1, 64, dtype=BF)), SHAPE),
+    (dict(rows=1, x=torch.zeros(64, dtype=BF), y=torch.zeros(1, 1, 64, dtype=BF)), OK),
+    (dict(rows=1, x=torch.zeros(1, 1, dtype=BF).expand(1, 64)), SHAPE),
+    (dict(rows=1, x=torch.zeros(1, 128, dtype=BF)[:, ::2]), SHAPE),
+    (dict(rows=21), SHAPE),
+], ids=ids)
+def test_norm_forward(bad, want):
+    with RmsNorm(20, 64, "bf16", ld=72, ldy=72) as n:
+        assert status(n.forward, **norm_args() | bad) == want
+
+
+def test_norm_scales():
+    a = dict(x=room(20, 64), gamma=torch.zeros(64, dtype=BF), y=room(20, 64, E4, 16))
+    with RmsNorm(20, 64, "bf16", out="mx", ld=72, ldy=80) as n:
+        s = torch.zeros(20, n.scale_ld, dtype=torch.uint8)
+        assert status(n.forward, **a, scales=s) == OK
+        assert status(n.forward, **a, scales=s.view(torch.float8_e8m0fnu)) == OK
+        assert status(n.forward, **a, scales=s[:, :2]) == SHAPE
+        assert status(n.forward, **a, scales=s[:19]) == SHAPE
+        assert status(n.forward, **a, scales=torch.zeros(1 << 12)) == DTYPE
+
+
+@pytest.mark.parametrize("bad,want", [
+    ({}, OK),
+    (dict(dy=torch.ones(1, dtype=BF).expand(20, 64)), SHAPE),         # the gradient of a sum
+    (dict(h=room(20, 136)[:, ::2]), SHAPE),
+    (dict(dh=room(19, 64)), SHAPE),
+    (dict(dx=torch.zeros(20, 64, dtype=BF)), SHAPE),                  # as empty_like of a padded view gives
+    (dict(dx=room(20, 64, torch.float32)), DTYPE),
+    (dict(dx=None), B.GE_ERR_NULL),
+    (dict(rstd=torch.zeros(1).expand(20)), SHAPE),
+    (dict(dgamma=torch.zeros(64)), DTYPE),
+    (dict(workspace=None), B.GE_ERR_WORKSPACE),
+    (dict(workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 20)), SHAPE),
+    (dict(rows=0, dy=None, h=None, rstd=None, dx=None, dh=None), OK),
+], ids=ids)
+def test_norm_backward(bad, want):
+    a = dict(dy=room(20, 64), h=room(20, 64), gamma=torch.zeros(64, dtype=BF), rstd=torch.zeros(20), dx=room(20, 64),
+             dgamma=torch.zeros(64, dtype=BF), dh=room(20, 64), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+    with RmsNorm(20, 64, "bf16", ld=72, ldy=72) as n:
+        assert status(n.backward, **a | bad) == want
+
+
+def test_norm_off_the_gpu(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    with RmsNorm(20, 64, "bf16", ld=72, ldy=72) as n:
+        with pytest.raises(B.GemmEpilogError, match="not on a GPU"):
+            n.forward(**norm_args())
