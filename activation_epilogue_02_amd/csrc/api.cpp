@@ -908,6 +908,9 @@ int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const vo
         !aligned(a_scales, 16) || !aligned(b_scales, 16) || !aligned(residual, 16) || !aligned(col_scale, 16) ||
         !aligned(workspace, 16) || !aligned(row_scale, 4) || !aligned(scale_a, 4) || !aligned(scale_b, 4))
         return GE_ERR_ALIGN;
+    // in place each value has to lie where it is written: with another stride a row of D
+    // would overwrite rows of R that other workgroups still read
+    if (residual && residual == D && ldr != d.ldd && m > 1) return GE_ERR_SHAPE;
     const size_t need = h->ws_partial + h->ws_counters;
     if (need > 0 && (!workspace || workspace_bytes < need)) return GE_ERR_WORKSPACE;
     if (test_fail_launch()) return GE_ERR_HIP;

@@ -439,13 +439,15 @@ int gemm_epilog_execute_mx(ge_handle h, const void* A, const void* B, const void
  *   a_scales, b_scales   block scales of GE_MXF8_E4M3 operands (see
  *                        execute_mx), NULL for every other type
  *   residual, ldr        R, m x n in D's type with row stride ldr elements;
- *                        NULL = 0.  R may be D itself (each value is read
- *                        before it is written, by the same thread).
+ *                        NULL = 0.  R may be D itself, with ldr == ldd (each
+ *                        value is read before it is written, by the same
+ *                        thread); no other overlap.
  *   row_scale, col_scale device fp32, m and n values; NULL = 1.  Any type.
  *   the others           as for execute
  * Alignment as for execute; col_scale 16 bytes, row_scale 4.
  * Errors: those of execute; GE_ERR_STATE (not planned for it); GE_ERR_SHAPE
- * (m, or ldr < n); GE_ERR_DTYPE (block scales for a type without). */
+ * (m, ldr < n, or R = D with another stride); GE_ERR_DTYPE (block scales for a
+ * type without). */
 int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis);
 int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const void* B, const void* a_scales,
                                  const void* b_scales, const void* bias, const void* residual, int64_t ldr,

@@ -190,3 +190,15 @@ def test_null_handles():
     assert L.gemm_epilog_plan_backward(None) == B.GE_ERR_NULL
     assert L.gemm_epilog_backward_workspace_size(None, ctypes.byref(ctypes.c_size_t())) == B.GE_ERR_NULL
     assert L.gemm_epilog_backward(None, *[None] * 8, 0, None) == B.GE_ERR_NULL
+
+
+def test_in_place_needs_the_same_rows(monkeypatch):
+    """R = D with another row stride: rows of D would overwrite rows of R that are still to be read."""
+    monkeypatch.setenv("GE_TEST_FAIL_LAUNCH", "1")
+    for m in (100, 20):                 # tiles, few rows
+        with handle(m, ldd=64) as g:
+            g.plan_residual("bias")
+            assert ex(g, R=P, ldr=64) == B.GE_ERR_HIP
+            assert ex(g, R=P, ldr=72) == B.GE_ERR_SHAPE
+            assert ex(g, R=P, ldr=72, m=1) == B.GE_ERR_HIP      # one row: nothing else to overwrite
+            assert ex(g, R=P + (1 << 24), ldr=72) == B.GE_ERR_HIP
