@@ -87,6 +87,11 @@ int ge_rms_norm_forward(ge_norm_handle h, int64_t rows, const void* x, const voi
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(hsum, 16) || !aligned(y, 16) ||
         !aligned(scales, d.out == GE_NORM_MX ? 16 : 4) || !aligned(rstd, 4))
         return GE_ERR_ALIGN;
+    // in place each value has to lie where it is written: with other rows (a stride of its own, or
+    // 8-bit ones) y would overwrite rows that other workgroups still read
+    if (rows > 0 && (y == x || y == residual || y == hsum) &&
+        (d.out != GE_NORM_PLAIN || (d.ldy != d.ld && rows > 1)))
+        return GE_ERR_SHAPE;
     if (test_fail_launch()) return GE_ERR_HIP;
     if (rows == 0) return GE_OK;
     NormArgs a = {};

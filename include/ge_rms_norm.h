@@ -76,9 +76,11 @@ int ge_rms_norm_workspace_size(ge_norm_handle h, size_t* bytes);
  *   scales     E4M3_ROW: rows fp32 values; MX: the scale bytes, 16-byte
  *              aligned; PLAIN: NULL
  *   rstd       rows fp32 values for the backward pass, or NULL
- * h may be x or residual itself, and a PLAIN y may be any of them (each value
- * is read before it is written, by the same thread); no other overlap.
- * Errors: GE_ERR_NULL, GE_ERR_SHAPE, GE_ERR_ALIGN (a matrix or gamma that is
+ * h may be x or residual itself, and a PLAIN y with ldy == ld may be any of
+ * them (each value is read before it is written, by the same thread); no
+ * other overlap.
+ * Errors: GE_ERR_NULL, GE_ERR_SHAPE (rows, or a y in place with rows of its
+ * own), GE_ERR_ALIGN (a matrix or gamma that is
  * not 16-byte aligned, scales or rstd not 4-byte aligned), GE_ERR_EPILOG
  * (scales or h given or missing against the rules above), GE_ERR_HIP. */
 int ge_rms_norm_forward(ge_norm_handle h, int64_t rows, const void* x, const void* residual, const void* gamma,

@@ -172,3 +172,22 @@ def test_wrapper_refuses_short_and_wrong_vectors():
         with pytest.raises(B.GemmEpilogError) as e:
             n.forward(ok, gamma, codes, scales=scales)
         assert e.value.status == B.GE_ERR_DTYPE
+
+
+@pytest.mark.parametrize("out,ldy,want", [(0, 64, B.GE_ERR_HIP), (0, 72, B.GE_ERR_SHAPE), (1, 64, B.GE_ERR_SHAPE),
+                                          (2, 128, B.GE_ERR_SHAPE)])
+def test_in_place_needs_the_same_rows(out, ldy, want, monkeypatch):
+    """y over x, the residual or h with rows of its own would overwrite rows that are still to be read."""
+    monkeypatch.setenv("GE_TEST_FAIL_LAUNCH", "1")
+    st, h = create(out=out, ldy=ldy)
+    assert st == B.GE_OK
+    Q, S = P + (1 << 20), P + (2 << 20)
+    sc = S if out else None
+    assert forward(h, x=P, y=Q, scales=sc) == B.GE_ERR_HIP
+    assert forward(h, x=P, y=P, scales=sc) == want
+    assert forward(h, x=P, res=Q, y=Q, scales=sc) == want
+    assert forward(h, x=P, res=Q, hs=S + (1 << 20), y=S + (1 << 20), scales=sc) == want
+    assert forward(h, x=P, res=Q, hs=P, y=S + (1 << 20), scales=sc) == B.GE_ERR_HIP    # h over x: one stride
+    if out == 0:
+        assert forward(h, rows=1, x=P, y=P) == B.GE_ERR_HIP                            # one row: nothing else
+    B.lib().ge_rms_norm_free(h)
