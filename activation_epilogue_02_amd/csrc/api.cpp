@@ -130,6 +130,17 @@ const TileShape* find_res_tile(int id) {
     return nullptr;
 }
 
+// The pipelined kernels' direct copies address a tile's rows of A, and of B
+// (either layout), as 32-bit offsets from the tile's first row or column:
+// the span must stay below 4 GiB.  (A K step is at most 128 elements.)
+bool tile_span_ok(const TileShape* t, const ge_desc& d) {
+    if (t->kernel == 1 || t->kernel == 3) return true;   // per-lane 64-bit addresses
+    const int64_t es = elem_size(d.a_type), lim = (int64_t)1 << 32;
+    if ((int64_t)t->bm * d.lda * es > lim) return false;
+    if (d.op_b == GE_OP_T) return (int64_t)t->bn * d.ldb * es <= lim;
+    return ((int64_t)128 * d.ldb + t->bn) * es <= lim;
+}
+
 // What a tile of the residual product costs: `fixed` us a round (prologue and
 // epilogue) and us per 128 bytes of K, in a full round of `slots` workgroups
 // and in one at most half full.
@@ -138,7 +149,8 @@ struct TileCost {
     double fixed, full, half;
 };
 
-// The tile of the least estimated time: tiles come in rounds of as many as the
+// The tile of the least estimated time among those whose rows lie close enough
+// together (0: none): tiles come in rounds of as many as the
 // chip holds, so 581 tiles of 64 x 64 take as long as 1024 would, and fewer,
 // larger ones win.  The figures are fits to the measured (bias, residual, 16-bit
 // output; us, estimate in brackets):
@@ -154,10 +166,11 @@ int cheapest_tile(const TileCost* t, int n, const ge_desc& d) {
     int best = 0;
     double least = 0.0;
     for (int i = 0; i < n; ++i) {
+        if (!tile_span_ok(find_res_tile(t[i].id), d)) continue;   // rows too far apart for it: the next one
         const int64_t tiles = ceil_div(d.m, t[i].bm) * ceil_div(d.n, t[i].bn), rest = tiles % t[i].slots;
         double us = (double)(tiles / t[i].slots) * (t[i].fixed + steps * t[i].full);
         if (rest > 0) us += t[i].fixed + steps * (2 * rest <= t[i].slots ? t[i].half : t[i].full);
-        if (i == 0 || us < least) {
+        if (best == 0 || us < least) {
             best = t[i].id;
             least = us;
         }
@@ -181,7 +194,8 @@ int choose_res_tile(const ge_desc& d) {
     case GE_F32: return t128 >= 256 ? 2 : 1;
     case GE_MXF8_E4M3: return t128 > 256 ? 19 : 18;
     case GE_F8_E4M3:
-        return ceil_div(d.m, 256) * ceil_div(d.n, 256) >= 512 ? 16 : cheapest_tile(k8, 3, d);
+        return ceil_div(d.m, 256) * ceil_div(d.n, 256) >= 512 && tile_span_ok(find_res_tile(16), d)
+                   ? 16 : cheapest_tile(k8, 3, d);
     }
     return cheapest_tile(k16, 3, d);
 }
@@ -264,17 +278,6 @@ int choose_tile(int64_t m, int64_t n, int a_type, int d_type) {
         return 13;   // small problems: 64 x 64 tiles, four deep stages
     }
     return choose_tile_plain(m, n);
-}
-
-// The pipelined kernels' direct copies address a tile's rows of A, and of B
-// (either layout), as 32-bit offsets from the tile's first row or column:
-// the span must stay below 4 GiB.  (A K step is at most 128 elements.)
-bool tile_span_ok(const TileShape* t, const ge_desc& d) {
-    if (t->kernel == 1 || t->kernel == 3) return true;   // per-lane 64-bit addresses
-    const int64_t es = elem_size(d.a_type), lim = (int64_t)1 << 32;
-    if ((int64_t)t->bm * d.lda * es > lim) return false;
-    if (d.op_b == GE_OP_T) return (int64_t)t->bn * d.ldb * es <= lim;
-    return ((int64_t)128 * d.ldb + t->bn) * es <= lim;
 }
 
 // Tile rows per group of the launch order (see tile_coords).  The 32 tiles
@@ -855,7 +858,7 @@ int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis) {
         q.path = PATH_TILE;
         q.tile_id = choose_res_tile(d);
         const TileShape* t = find_res_tile(q.tile_id);
-        if (!tile_span_ok(t, d)) return GE_ERR_SHAPE;
+        if (!t || !tile_span_ok(t, d)) return GE_ERR_SHAPE;
         const int64_t tm = ceil_div(d.m, t->bm), tn = ceil_div(d.n, t->bn);
         if (tm * tn > INT32_MAX) return GE_ERR_SHAPE;
         q.tiles_m = (int32_t)tm;

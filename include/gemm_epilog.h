@@ -433,7 +433,8 @@ int gemm_epilog_execute_mx(ge_handle h, const void* A, const void* B, const void
  * combination of ge_desc but an E4M3 D; one product (batch 0 or 1).
  * workspace_size, aux_ld and describe then answer for this plan.
  * Errors: GE_ERR_NULL; GE_ERR_EPILOG (another epilogue or axis); GE_ERR_SHAPE
- * (a batch, or a tile whose rows span 4 GiB or more); GE_ERR_DTYPE (E4M3 D).
+ * (a batch, or rows so far apart that every tile's span 4 GiB); GE_ERR_DTYPE
+ * (E4M3 D).
  *
  * gemm_epilog_execute_residual launches it for m rows, 0 <= m <= the planned.
  *   a_scales, b_scales   block scales of GE_MXF8_E4M3 operands (see

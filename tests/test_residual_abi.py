@@ -202,3 +202,26 @@ def test_in_place_needs_the_same_rows(monkeypatch):
             assert ex(g, R=P, ldr=72) == B.GE_ERR_SHAPE
             assert ex(g, R=P, ldr=72, m=1) == B.GE_ERR_HIP      # one row: nothing else to overwrite
             assert ex(g, R=P + (1 << 24), ldr=72) == B.GE_ERR_HIP
+
+
+@pytest.mark.parametrize("a,m,n,lda,want", [
+    # rows of 16, 32 and 64 MiB and more: 256, 128 and 64 of them are 4 GiB
+    ("bf16", 8192, 4096, 1 << 23, "tile_id=6 "),
+    ("bf16", 8192, 4096, 1 << 24, "tile_id=8 "),
+    ("bf16", 8192, 4096, 1 << 25, "tile_id=14 "),
+    ("bf16", 8192, 4096, 1 << 26, None),
+    ("f16", 100, 64, 1 << 25, "tile_id=14 "),
+    ("e4m3", 8192, 4096, 1 << 24, "tile_id=16 "),
+    ("e4m3", 8192, 4096, 1 << 25, "tile_id=8 "),
+    ("e4m3", 8192, 4096, 1 << 26, "tile_id=17 "),
+    ("e4m3", 8192, 4096, 1 << 27, None),
+    ("mxf8", 8192, 4096, 1 << 25, "tile_id=19 "),
+    ("mxf8", 8192, 4096, 1 << 26, None),
+    ("f32", 8192, 4096, 1 << 30, "tile_id=2 "),
+])
+def test_rows_far_apart(a, m, n, lda, want):
+    """A tile that cannot address its rows leaves the choice to a smaller one."""
+    with handle(m, n, 64, a, lda=lda) as g:
+        assert status(g.plan_residual, "bias") == (B.GE_ERR_SHAPE if want is None else B.GE_OK)
+        if want is not None:
+            assert want in g.describe() + " ", g.describe()
