@@ -150,6 +150,27 @@ __device__ __forceinline__ float row_scale(float a) {
     return a > 0.0f ? __builtin_fmaxf(a / 448.0f, 0x1p-126f) : 1.0f;
 }
 
+// y / s, rounded once (2^-24): the codes are those of the quotient.  A product
+// with 1 / s lands beside the quotient for about every fourth value, and codes
+// of values next to a border between two of them then differ.  With both scaled
+// so that s is in [1, 2), which is exact, q = y * inv is off by an ulp or two,
+// its remainder y - q s is exact, and one step with it rounds correctly (checked
+// against divisions for 4e7 values, at and next to borders too).  s = inf gives 0,
+// and NaN for infinite y, as the division does.
+struct RowQuotient {
+    float pow2, s, inv;
+};
+__device__ __forceinline__ RowQuotient row_quotient(float s) {
+    if (s == __builtin_inff()) return {0.0f, 1.0f, 1.0f};
+    const float pow2 = __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);   // s is normal and below 2^120
+    return {pow2, s * pow2, 1.0f / (s * pow2)};
+}
+__device__ __forceinline__ float divide(float y, const RowQuotient& d) {
+    y *= d.pow2;
+    const float q = y * d.inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, d.s, y), d.inv, q);
+}
+
 // The squared sum's rstd.
 __device__ __forceinline__ float rstd_of(float ss, const NormArgs& p) { return 1.0f / sqrtf(ss * p.inv_cols + p.eps); }
 
@@ -216,14 +237,14 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_fwd(NormArgs p) {
             slot ^= 1;
         } else if constexpr (OUT == GE_NORM_E4M3_ROW) {
             amax = row_reduce<T, true>(amax, red, 1);
-            const float s = row_scale(amax), f = 1.0f / s;
+            const float s = row_scale(amax);
+            const RowQuotient d = row_quotient(s);
             if (t == 0) ((float*)p.scales)[row] = s;
             uint8_t* y = (uint8_t*)p.y + row * p.ldy;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                // (two roundings of 2^-24: far below a step of the codes)
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[i][e] *= f;
+                for (int e = 0; e < E; ++e) v[i][e] = divide(v[i][e], d);
                 if (t + i * T < C) store_codes<E, false>(y, t + i * T, cols, v[i]);
             }
         } else {
@@ -307,6 +328,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long(NormArgs p) {
             s = row_scale(amax);
             if (t == 0) ((float*)p.scales)[row] = s;
         }
+        [[maybe_unused]] const RowQuotient d = row_quotient(s);
         // every lane of a block's group takes part in its exchange, so the loop
         // runs to the same count in all of them
         for (int64_t c0 = 0; c0 < C; c0 += T) {
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long(NormArgs p) {
                 if (in) store_chunk<DT>((uint8_t*)p.y + row * p.ldy * ES, c, cols, v);
             } else if constexpr (OUT == GE_NORM_E4M3_ROW) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] *= 1.0f / s;
+                for (int e = 0; e < E; ++e) v[e] = divide(v[e], d);
                 if (in) store_codes<E, false>((uint8_t*)p.y + row * p.ldy, c, cols, v);
             } else {
                 float a = 0.0f, f;

@@ -338,3 +338,44 @@ def test_tiny_rows_keep_a_normal_scale():
     assert (s == 2.0 ** -126).all() and (y[0].float() == 0).all()
     # 3e-37 * 2^126 = 25.5: the nearest code is 26
     assert (y[1].float() == 26).all()
+
+
+@pytest.mark.parametrize("dtype,cols", [("f32", 1024), ("f32", 32768), ("f16", 512), ("f16", 65536), ("bf16", 256),
+                                        ("bf16", 8192), ("bf16", 65536)])
+def test_codes_are_those_of_the_quotient(dtype, cols):
+    """Rows of +-1 with eps = 0 have rstd = 1 exactly, so y = +-gamma.  With gamma = c s for c half way between
+    two codes and 448 s the largest, y / s = c exactly and the codes are c rounded to even."""
+    t = DT[dtype]
+    c = torch.tensor([(2 * j + 1) / 32 * 2.0 ** e for j in range(8, 16) for e in range(-5, 9)], dtype=torch.float64)
+    c = torch.cat([c[c < 448], torch.tensor([448.0], dtype=torch.float64)])
+    c = c.repeat(cols // len(c) + 1)[:cols]
+    want = c.to(torch.float8_e4m3fn).float()
+    sign = torch.where(torch.arange(cols) % 3 == 0, -1.0, 1.0)
+    scales = {"bf16": [1.25, 1.5, 1.75, 0.75, 40.0], "f16": [1 + i / 16 for i in range(1, 16)],
+              "f32": [1 + i / 512 for i in range(3, 512, 20)] + [1.7 * 2.0 ** -110, 1.3 * 2.0 ** 100]}[dtype]
+    if dtype == "f32":
+        scales = [float(torch.tensor(s, dtype=torch.float32).view(torch.int32).bitwise_and(-4096).view(torch.float32))
+                  for s in scales]   # 12 bits: c s is exact
+    with RmsNorm(2, cols, dtype, out="e4m3_row", eps=0.0) as n:
+        x = (sign * torch.tensor([[1.0], [-1.0]])).to(t).cuda()
+        y, row_scale = n.alloc_outputs()
+        for s in scales:
+            gamma = (c * s).to(t)
+            assert torch.equal(gamma.double(), c * s)
+            n.forward(x, gamma.cuda(), y, scales=row_scale)
+            assert (row_scale.double().cpu() == s).all(), s
+            got = y.float().cpu()
+            assert torch.equal(got[0], sign * want) and torch.equal(got[1], -sign * want), s
+
+
+def test_infinite_values_with_a_row_scale():
+    """gamma so large that a value of y is infinite: the scale is infinite, that code NaN and the others zero."""
+    gamma = torch.ones(64, device="cuda")
+    gamma[5] = 3e38
+    x = torch.zeros(1, 64, device="cuda")
+    x[0, :8] = torch.arange(1, 9, device="cuda")
+    with RmsNorm(1, 64, "f32", out="e4m3_row", eps=0.0) as n:
+        y, s = n.alloc_outputs()
+        n.forward(x, gamma, y, scales=s)
+    y = y.float()
+    assert s.isinf().all() and y[0, 5].isnan() and (y[0, :5] == 0).all() and (y[0, 6:] == 0).all()
