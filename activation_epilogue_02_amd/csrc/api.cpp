@@ -72,7 +72,8 @@ struct ge_plan_s {
     const float* scale_d = nullptr;   // fp8 output: D's scale (NULL = 1)
     float* amax_d = nullptr;          // fp8 output: largest |y| per product, or NULL
     // residual product (gemm_epilog_plan_residual): the plan is for
-    // execute_residual only; skinny_mb = row groups of the streaming kernel
+    // execute_residual only; skinny_mb = row groups of the streaming kernel (at the
+    // planned rows: a call takes the shape of its own)
     bool residual = false;
     int32_t skinny_mb = 0;
     // its backward pass (gemm_epilog_plan_backward): dP (bytes, row stride),
@@ -820,6 +821,18 @@ int gemm_epilog_execute_static(ge_handle h, const void* A, const void* B, const 
 }
 
 // ---- residual product ---------------------------------------------------------
+// Few rows and a weight given n x k: W is streamed once.
+static bool few_rows(const ge_desc& d, int64_t m) { return m <= 64 && d.op_b == GE_OP_T && d.a_type != GE_F32; }
+
+// The streaming kernel for m rows: groups of 16 rows and of 16 columns per workgroup.
+struct FewRowsShape {
+    int32_t mb, rg, blocks;
+};
+static FewRowsShape few_rows_shape(const ge_desc& d, int64_t m) {
+    const int32_t rg = ceil_div(d.n, 32) >= 256 ? 2 : 1;
+    return {m <= 16 ? 1 : m <= 32 ? 2 : 4, rg, (int32_t)ceil_div(d.n, 16 * rg)};
+}
+
 int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis) {
     if (!h) return GE_ERR_NULL;
     const bool known = epilog == GE_EPILOG_NONE || has_bias(epilog);
@@ -845,15 +858,15 @@ int gemm_epilog_plan_residual(ge_handle h, int32_t epilog, int32_t bias_axis) {
               : aux_is_matrix(epilog) ? (int64_t)round_up((size_t)d.n, 128)
                                       : (int64_t)round_up((size_t)d.n, 128) / 32;
     if (q.ldaux > INT32_MAX) return GE_ERR_SHAPE;
-    if (d.m <= 64 && d.op_b == GE_OP_T && d.a_type != GE_F32) {
-        // few rows and a weight given n x k: W is streamed once
+    if (few_rows(d, d.m)) {
+        const FewRowsShape f = few_rows_shape(d, d.m);
         q.path = PATH_SKINNY;
         q.tile_id = 0;
-        q.skinny_mb = d.m <= 16 ? 1 : d.m <= 32 ? 2 : 4;
-        q.group_m = ceil_div(d.n, 32) >= 256 ? 2 : 1;
+        q.skinny_mb = f.mb;
+        q.group_m = f.rg;
         q.tiles_m = 1;
-        q.tiles_n = (int32_t)ceil_div(d.n, 16 * q.group_m);
-        q.grid = (unsigned)q.tiles_n;
+        q.tiles_n = f.blocks;
+        q.grid = (unsigned)f.blocks;
     } else {
         q.path = PATH_TILE;
         q.tile_id = choose_res_tile(d);
@@ -953,9 +966,15 @@ int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const vo
     r.row_scale = row_scale;
     r.col_scale = col_scale;
     r.ldr = ldr;
-    if (h->path == PATH_SKINNY)
-        return launch_skinny(d.a_type, d.d_type, h->skinny_mb, h->group_m, a, r, h->grid, stream) == 0 ? GE_OK
-                                                                                                      : GE_ERR_HIP;
+    // by this call's rows, not the plan's: a handle for prompts serves single tokens too, and
+    // its tiles would walk all of K in a few workgroups
+    if (few_rows(d, m)) {
+        const FewRowsShape f = few_rows_shape(d, m);
+        a.tiles_m = 1;
+        a.tiles_n = f.blocks;
+        return launch_skinny(d.a_type, d.d_type, f.mb, f.rg, a, r, (unsigned)f.blocks, stream) == 0 ? GE_OK
+                                                                                                    : GE_ERR_HIP;
+    }
     unsigned grid = h->grid;
     if (m != d.m) {
         a.tiles_m = (int32_t)ceil_div(m, find_res_tile(h->tile_id)->bm);

@@ -450,3 +450,34 @@ def test_streams_and_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), i
     g.free()
+
+
+@pytest.mark.parametrize("a,d", COMBOS, ids=IDS)
+@pytest.mark.parametrize("planned", [64, 70, 300])
+def test_few_rows_of_a_larger_plan(a, d, planned):
+    """A call's kernel follows its own rows: the bits are those of a handle planned for them."""
+    n, k = 200, 4100
+    randn = gen(21)
+    A, W, R = laid(randn(planned, k), a), laid(randn(n, k), a), laid(randn(planned, n), d)
+    sa, sb = (block_scales(r, k, randn)[0] if a == "mxf8" else None for r in (planned, n))
+    rs, cs = torch.exp(0.5 * randn(planned)), torch.exp(0.5 * randn(n))
+    bias = randn(n).to(DT[d])
+    for kind in ("relu_aux_bias", "gelu_aux_bias"):
+        for rows in (1, 16, 17, 33, 64):
+            outs = []
+            for size in (planned, rows):
+                print(f"case {a}->{d} {kind} rows={rows} planned={size}", flush=True)
+                D = laid(torch.zeros(planned, n, device="cuda"), d)
+                before = D.clone()
+                with GemmEpilog(size, n, k, a, d, GE_OP_T, A.stride(0), W.stride(0), D.stride(0)) as g:
+                    g.plan_residual(kind)
+                    aux = (torch.full((planned, g.aux_ld_bits // 32), -1, dtype=torch.int32, device="cuda")
+                           if kind == "relu_aux_bias" else
+                           torch.full((planned, g.aux_ld_bits // torch.finfo(DT[d]).bits), 3.0, dtype=DT[d], device="cuda"))
+                    aux0 = aux.clone()
+                    ws = torch.full((max(1, g.ws_bytes),), 0xA5, dtype=torch.uint8, device="cuda")
+                    g.execute_residual(A, W, bias, R, D, aux=aux, row_scale=rs, col_scale=cs, a_scales=sa, b_scales=sb,
+                                       workspace=ws, m=rows)
+                assert untouched(D) and torch.equal(D[rows:], before[rows:]) and torch.equal(aux[rows:], aux0[rows:])
+                outs.append((D[:rows].clone(), aux[:rows].clone()))
+            assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1]), rows
