@@ -266,3 +266,19 @@ def test_norm_off_the_gpu(monkeypatch):
     with RmsNorm(20, 64, "bf16", ld=72, ldy=72) as n:
         with pytest.raises(B.GemmEpilogError, match="not on a GPU"):
             n.forward(**norm_args())
+
+
+def test_stream_without_internal_calls(monkeypatch):
+    """A torch that lacks the internal calls gives the stream by its public object."""
+    import importlib.util
+    import types
+
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("binding_again", B.__file__)
+    fresh = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fresh)
+    assert fresh._stream(None) is None and fresh._stream(7) == 7      # (no GPU in use)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=0x1234))
+    assert fresh._stream(None) == 0x1234
