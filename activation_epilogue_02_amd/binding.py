@@ -216,10 +216,13 @@ def _workspace(t, device, what):
 
 
 def _device(t, what) -> int:
-    """The GPU of a call's output; the call's other tensors have to share it."""
+    """The GPU of a call's output: the current one, where the launch goes; the call's other tensors share it."""
     d = t.get_device()
-    if d < 0 and torch.cuda.is_available():   # (without a GPU the launch itself reports that)
-        raise GemmEpilogError(GE_ERR_HIP, what + " is not on a GPU")
+    if d < 0:
+        if torch.cuda.is_available():   # (without a GPU the launch itself reports that)
+            raise GemmEpilogError(GE_ERR_HIP, what + " is not on a GPU")
+    elif d != (torch.cuda.current_device() if _raw_device is None else _raw_device()):
+        raise GemmEpilogError(GE_ERR_HIP, what + " is not on the current GPU")
     return d
 
 
@@ -491,7 +494,8 @@ class GemmEpilog:
         """residual is an m x n matrix in D's dtype (any 16-byte row stride), or None; m: rows of this call.
 
         Every tensor has to hold what the call reads or writes, in the planned types and row strides:
-        GemmEpilogError with GE_ERR_DTYPE or GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on D's GPU)."""
+        GemmEpilogError with GE_ERR_DTYPE or GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on the
+        current GPU, whose stream takes the launch)."""
         if D is None:
             D, aux_new, ws_new = self.alloc_outputs(A.device)
             aux = aux if aux is not None else aux_new

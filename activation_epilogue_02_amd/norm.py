@@ -60,7 +60,7 @@ class RmsNorm:
         """Writes y (and scales, h, rstd where given) for `rows` rows.
 
         Every tensor has to hold those rows in the handle's types and strides: GemmEpilogError with GE_ERR_DTYPE or
-        GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on y's GPU)."""
+        GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on the current GPU, whose stream takes the launch)."""
         n, cols, ld, t = self.rows if rows is None else rows, self.cols, self.ld, self.dtype
         first = y if y is not None else gamma   # (the library refuses what is missing)
         dev = -1 if first is None else _device(first, "RmsNorm.forward: y")

@@ -282,3 +282,17 @@ def test_stream_without_internal_calls(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=0x1234))
     assert fresh._stream(None) == 0x1234
+
+
+def test_tensors_of_another_gpu(monkeypatch):
+    """The launch goes to the current GPU's stream: another one's memory is refused."""
+    class On:
+        def __init__(self, d):
+            self.get_device = lambda: d
+    monkeypatch.setattr(B, "_raw_device", lambda: 1)
+    assert B._device(On(1), "x") == 1
+    with pytest.raises(B.GemmEpilogError, match="current GPU"):
+        B._device(On(0), "x")
+    monkeypatch.setattr(B, "_raw_device", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert B._device(On(0), "x") == 0
