@@ -14,6 +14,14 @@ namespace {
 
 constexpr int TS = 64;   // tile rows and columns
 
+// GELU' of a stored pre-activation.  One that left the type's range is stored as an
+// infinity (fp16: beyond 65504), where the formula is inf * 0: beyond 30 GELU' is 1 or 0
+// to the last bit of fp32, so the argument is cut there.  NaN stays NaN.
+__device__ __forceinline__ float gelu_slope(float x) {
+    x = x > 30.0f ? 30.0f : x;
+    return gelu_tanh_deriv(x < -30.0f ? -30.0f : x);
+}
+
 template <int DT, int KIND>
 __global__ void __launch_bounds__(256) grad_prepare(GradArgs p) {
     constexpr int E = 16 / Elem<DT>::size, CH = TS / E, RP = 256 / CH;   // rows per pass
@@ -69,7 +77,7 @@ __global__ void __launch_bounds__(256) grad_prepare(GradArgs p) {
                     for (int e = 0; e < E; ++e) pre[e] = n + e < N ? ax[e] : (T)0;
                 }
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] *= gelu_tanh_deriv(load_scalar<DT>(pre, e));
+                for (int e = 0; e < E; ++e) v[e] *= gelu_slope(load_scalar<DT>(pre, e));
             }
             if constexpr (KIND == GRAD_MASK || KIND == GRAD_GELU) {
                 // dP is rounded to the operands' type: the products take it in 16 bits

@@ -461,7 +461,9 @@ int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const vo
 
 /* Backward pass of the residual product, for the planned m rows and without
  * scales (training runs in 16 or 32 bits):
- *   dP = dD * act'(aux)          (RELU_AUX_BIAS, GELU_AUX_BIAS; else dP = dD)
+ *   dP = dD * act'(aux)          (RELU_AUX_BIAS, GELU_AUX_BIAS; else dP = dD;
+ *                                 GELU' of an aux beyond its type's range, stored
+ *                                 as an infinity, is its limit 0 or 1)
  *   dA = dP B^T,  dB = A^T dP in B's own layout,  dbias = sums of dP
  *   (the residual's gradient is dD itself)
  * gemm_epilog_plan_backward follows plan_residual with NONE, BIAS,

@@ -481,3 +481,33 @@ def test_few_rows_of_a_larger_plan(a, d, planned):
                 assert untouched(D) and torch.equal(D[rows:], before[rows:]) and torch.equal(aux[rows:], aux0[rows:])
                 outs.append((D[:rows].clone(), aux[:rows].clone()))
             assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1]), rows
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "f32"])
+def test_gelu_gradient_of_stored_infinities(t):
+    """The forward pass of P = -1e5 and below is finite, and fp16 stores that P as -inf: GELU' there is 0, at +inf 1,
+    and at the type's largest values as well; NaN stays NaN and in its own row and column."""
+    m, n, k = 40, 72, 48
+    randn = gen(31)
+    A, W, dD = laid(randn(m, k), t), laid(randn(n, k), t), laid(randn(m, n), t)
+    top = torch.finfo(DT[t]).max
+    aux = torch.zeros(m, 128, dtype=DT[t], device="cuda")
+    aux[:, :n] = torch.tensor([-float("inf"), float("inf"), -top, top, 31.0, -31.0, -29.0], device="cuda")[
+        torch.arange(m * n, device="cuda").view(m, n) % 7].to(DT[t])
+    slope = (aux[:, :n].double() > 0).double()
+    aux[3, 5] = float("nan")
+    dP = dD.double() * slope
+    gA, gB = laid(torch.zeros(m, k, device="cuda"), t), laid(torch.zeros(n, k, device="cuda"), t)
+    gb = torch.empty(n, dtype=DT[t], device="cuda")
+    with GemmEpilog(m, n, k, t, t, GE_OP_T, A.stride(0), W.stride(0), dD.stride(0)) as g:
+        g.plan_residual("gelu_aux_bias").plan_backward()
+        g.backward(dD, A, W, gA, gB, dbias=gb, aux=aux,
+                   workspace=torch.empty(g.backward_ws_bytes, dtype=torch.uint8, device="cuda"))
+    assert gA[3].isnan().all() and gB[5].isnan().all() and gb[5].isnan()
+    rows, cols = (torch.arange(s, device="cuda") != i for s, i in ((m, 3), (n, 5)))
+    f = torch.finfo(DT[t])
+    for got, want, size, terms in ((gA[rows], (dP @ W.double())[rows], (dP.abs() @ W.double().abs())[rows], n),
+                                   (gB[cols], (dP.t() @ A.double())[cols], (dP.abs().t() @ A.double().abs())[cols], m),
+                                   (gb[cols], dP.sum(0)[cols], dP.abs().sum(0)[cols], m)):
+        tol = size * (terms + 8) * U + want.abs() * f.eps / 2 * (1 + 2.0 ** -6) + f.tiny * f.eps
+        assert ((got.double() - want).abs() <= tol).all()
