@@ -511,3 +511,39 @@ def test_gelu_gradient_of_stored_infinities(t):
                                    (gb[cols], dP.sum(0)[cols], dP.abs().sum(0)[cols], m)):
         tol = size * (terms + 8) * U + want.abs() * f.eps / 2 * (1 + 2.0 ** -6) + f.tiny * f.eps
         assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("m", [1, 100])
+@pytest.mark.parametrize("a", ["e4m3", "mxf8"])
+def test_what_eight_bit_sums_keep(a, m):
+    """As the header says of 8-bit operands: beside 2^16, 8 counts in the same group of eight K values, and in another
+    group anything does; what is dropped is at most 7 2^-13 of the groups' largest products."""
+    k, n, big = 128, 128, 65
+    A, W = torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda")
+    A[:, big], W[:, big] = 256, 256
+    A[:, :] += torch.where(torch.arange(k, device="cuda") == big, 0.0, 2.0)
+    # row j of W: the product 2 w at K value j alone, w = 4 inside the group and 0.5 outside
+    j = torch.arange(n, device="cuda")
+    inside = j // 8 == big // 8
+    W[j, j] += torch.where(j == big, 0.0, torch.where(inside, 4.0, 0.5))
+    small = torch.where(inside, 8.0, 1.0).double()
+    small[big] = 0
+    sa, sb = (torch.full((r, mx_scale_ld(k)), 127, dtype=torch.uint8, device="cuda") if a == "mxf8" else None
+              for r in (m, n))
+    A, W = laid(A, a), laid(W, a)
+    D = laid(torch.zeros(m, n, device="cuda"), "f32")
+    with GemmEpilog(m, n, k, a, "f32", GE_OP_T, A.stride(0), W.stride(0), D.stride(0)) as g:
+        g.plan_residual("none")
+        ws = torch.empty(max(1, g.ws_bytes), dtype=torch.uint8, device="cuda")
+        g.execute_residual(A, W, None, None, D, a_scales=sa, b_scales=sb, workspace=ws)
+    assert torch.equal(D.double(), (65536.0 + small).expand(m, n))
+    # seven products just below the border in the group of the largest
+    W2 = torch.zeros(n, k, device="cuda")
+    W2[:, big] = 256
+    W2[:, 64:72] += torch.where(torch.arange(64, 72, device="cuda") == big, 0.0, 3.75)
+    W2 = laid(W2, a)
+    want = A.double() @ W2.double().t()
+    with GemmEpilog(m, n, k, a, "f32", GE_OP_T, A.stride(0), W2.stride(0), D.stride(0)) as g:
+        g.plan_residual("none")
+        g.execute_residual(A, W2, None, None, D, a_scales=sa, b_scales=sb, workspace=ws)
+    assert ((D.double() - want).abs() <= 7 * 2.0 ** -13 * 65536).all()
