@@ -55,3 +55,33 @@ def test_serving(tokens):
     # one row at a time gives what the batch gives, to the rounding of the output
     one = block(x[:1], r[:1]).clone()
     assert (one.double() - out[:1].double()).norm() <= 2.0 ** -4 * 2 ** 0.5 * (want[:1] - h[:1]).norm() + 2.0 ** -7 * h[:1].norm()
+
+
+@pytest.mark.parametrize("planned", [64, 200])
+@pytest.mark.parametrize("tokens", [1, 5, 17, 64, 65, 200])
+def test_one_token_against_the_batch(planned, tokens):
+    """A token alone against the same token in a batch.  Up to 64 rows both take the kernel for few rows, which adds
+    in one order whatever the rows: equal bits.  Beyond, the first product is added in another order (off by far less
+    than a rounding), so each u may round to a neighbour, a step of 2^-7 of it, and so may out."""
+    if tokens > planned:
+        pytest.skip("more tokens than planned")
+    d, f = 256, 520
+    args = ff.inputs(200, d, f, "bf16", 7)
+    block = ff.Serving(planned, *args[2:])
+    assert ("path=skinny" in block.up.describe()) == (planned <= 64)
+    x, r = args[0], args[1]
+    batch = block(x[:tokens], r[:tokens])[:1].clone()
+    u_batch = block.u[:1].double()
+    block.out.fill_(float("nan"))
+    block.u.fill_(float("nan"))
+    one = block(x[:1], r[:1]).clone()
+    u = block.u[:1].double()
+    assert one.shape == (1, d) and not one.isnan().any()
+    if tokens <= 64:
+        assert torch.equal(one, batch) and torch.equal(u, u_batch)
+        return
+    size = u.abs().maximum(u_batch.abs())
+    assert ((u - u_batch).abs() <= size * 2.0 ** -7 + 2.0 ** -20).all()
+    w2 = block.w2.double().abs()
+    tol = (size * 2.0 ** -7 + 2.0 ** -20) @ w2.t() + (f + 8) * 2.0 ** -24 * (size @ w2.t()) + 2.0 ** -7 * one.double().abs()
+    assert ((one.double() - batch.double()).abs() <= tol).all()

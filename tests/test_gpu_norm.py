@@ -379,3 +379,38 @@ def test_infinite_values_with_a_row_scale():
         n.forward(x, gamma, y, scales=s)
     y = y.float()
     assert s.isinf().all() and y[0, 5].isnan() and (y[0, :5] == 0).all() and (y[0, 6:] == 0).all()
+
+
+@pytest.mark.parametrize("planned,rows,cols", [(3000, 2100, 96), (3000, 3000, 200), (700, 300, 2055), (700, 1, 4104),
+                                               (400, 257, 8200), (600, 513, 1000), (40, 7, 40001)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_backward_of_fewer_rows(planned, rows, cols, dtype):
+    """0 < rows <= the handle's, with the workspace of the whole handle; dgamma under the bound of the launch: a group
+    adds its rows in turn, the groups of a workgroup one after the other, then 32 lanes every 32nd workgroup's sum, and
+    the 32 of them; each term is off by 3 roundings itself."""
+    t = DT[dtype]
+    h, dy, gamma = inputs(planned, cols, t, 1, cols + 5)
+    dh = inputs(planned, cols, t, 1, cols + 6)[0]
+    rstd = (1 / torch.sqrt((h.double() ** 2).mean(1) + EPS)).float()
+    dx, size, dg, dgsize = grads(dy[:rows], h[:rows], gamma, rstd[:rows], dh[:rows])
+    got = laid(torch.full((planned, cols), 3.0, device="cuda"), t, 1)
+    gg = torch.full((cols + 8,), 7.0, dtype=t, device="cuda")
+    with RmsNorm(planned, cols, dtype, eps=EPS, ld=h.stride(0)) as n:
+        threads = int(n.describe().split("backward=")[1].split("x")[0])
+        ws = torch.full((n.workspace_bytes,), 0xA5, dtype=torch.uint8, device="cuda")
+        n.backward(dy, h, gamma, rstd, got, gg[:cols], dh=dh, workspace=ws, rows=rows)
+    f = torch.finfo(t)
+    assert (got[rows:] == 3).all() and (gg[cols:] == 7).all()
+    tol = dx.abs() * f.eps / 2 * (1 + 2.0 ** -6) + size * K(cols) * U + f.tiny * f.eps
+    assert ((got[:rows].double() - dx).abs() <= tol).all()
+    blocks, groups = min(rows, 256), max(1, 512 // threads)
+    steps = -(-rows // (blocks * groups)) + groups + -(-blocks // 32) + 32 + 3
+    tol = dg.abs() * f.eps / 2 * (1 + 2.0 ** -6) + dgsize * steps * U + f.tiny * f.eps
+    assert ((gg[:cols].double() - dg).abs() <= tol).all()
+    # a handle of those rows gives the same bits
+    with RmsNorm(rows, cols, dtype, eps=EPS, ld=h.stride(0)) as n:
+        again = laid(torch.zeros(rows, cols, device="cuda"), t, 1)
+        g2 = torch.empty(cols, dtype=t, device="cuda")
+        n.backward(dy, h, gamma, rstd, again, g2, dh=dh, rows=rows,
+                   workspace=torch.empty(n.workspace_bytes, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(again, got[:rows]) and torch.equal(g2, gg[:cols])
