@@ -821,8 +821,27 @@ int gemm_epilog_execute_static(ge_handle h, const void* A, const void* B, const 
 }
 
 // ---- residual product ---------------------------------------------------------
-// Few rows and a weight given n x k: W is streamed once.
+// Few rows and a weight given n x k: W is streamed once.  Up to 64 rows, against
+// the split-K tiles (us, streaming / tiles, at 1, 32 and 64 rows):
+//   bf16 1024 x 1024 (n x k), 33 and 64 rows: 6.0 / 7.1, 6.4 / 7.3; 2048 x 2048: 8.0 / 10.6, 8.4 / 10.7
+//     4096 x 4096 9.8 / 14.9, 12.4 / 14.9, 16.5 / 15.4; 1024 x 8192 8.9 / 13.2, 13.2 / 13.4, 17.6 / 13.6
+//     4096 x 16384 31 / 37, 39 / 37, 50 / 38; 16384 x 4096 35 / 33, 37 / 33, 40 / 33
+//   E4M3 4096 x 4096 6.4 / 11.9, 7.9 / 12.2, 9.2 / 12.9; 4096 x 16384 15.2 / 25.1, 19.8 / 25.6, 24.8 / 26.0
+//   block-scaled 4096 x 4096 7.1 / 19.3, 8.8 / 19.8, 12.4 / 20.7; 4096 x 16384 15.7 / 35, 27 / 37, 41 / 38
+// The limit is one for every type, though with 33 rows and more of large 16-bit
+// weights the tiles win (x, read by every workgroup, is then more bytes than W).
 static bool few_rows(const ge_desc& d, int64_t m) { return m <= 64 && d.op_b == GE_OP_T && d.a_type != GE_F32; }
+
+// Whether a call of m rows streams.  Its own rows decide, not the plan's: a handle
+// for prompts serves single tokens too, and its tiles would walk all of K in a
+// few workgroups (1 x 4096 x 16384 bf16 on a handle of 8192 rows: 258 us, 30
+// streamed).  Only where the plan has the 64 x 64 split-K tiles and they are the
+// faster ones (above: 33 rows and more, from 16 MiB of weight on) they stay.
+static bool streams(const ge_plan_s* h, int64_t m) {
+    const ge_desc& d = h->d;
+    if (!few_rows(d, m)) return false;
+    return h->path == PATH_SKINNY || h->tile_id != 14 || m <= 32 || d.n * d.k * elem_size(d.a_type) < (int64_t)16 << 20;
+}
 
 // The streaming kernel for m rows: groups of 16 rows and of 16 columns per workgroup.
 struct FewRowsShape {
@@ -966,9 +985,7 @@ int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const vo
     r.row_scale = row_scale;
     r.col_scale = col_scale;
     r.ldr = ldr;
-    // by this call's rows, not the plan's: a handle for prompts serves single tokens too, and
-    // its tiles would walk all of K in a few workgroups
-    if (few_rows(d, m)) {
+    if (streams(h, m)) {
         const FewRowsShape f = few_rows_shape(d, m);
         a.tiles_m = 1;
         a.tiles_n = f.blocks;

@@ -547,3 +547,36 @@ def test_what_eight_bit_sums_keep(a, m):
         g.plan_residual("none")
         g.execute_residual(A, W2, None, None, D, a_scales=sa, b_scales=sb, workspace=ws)
     assert ((D.double() - want).abs() <= 7 * 2.0 ** -13 * 65536).all()
+
+
+@pytest.mark.parametrize("d", ["bf16", "f32"])
+def test_few_rows_of_a_split_k_plan(d):
+    """A 16-bit weight of 16 MiB on a handle of 100 rows, which has split-K tiles: from 33 rows on the call keeps them
+    (the bits of those rows in a full call), below it streams (the bits of a handle of those rows)."""
+    planned, n, k = 100, 1024, 8192
+    randn = gen(22)
+    A, W, R = laid(randn(planned, k), "bf16"), laid(randn(n, k), "bf16"), laid(randn(planned, n), d)
+
+    def call(size, rows):
+        D = laid(torch.zeros(planned, n, device="cuda"), d)
+        with GemmEpilog(size, n, k, "bf16", d, GE_OP_T, A.stride(0), W.stride(0), D.stride(0)) as g:
+            g.plan_residual("none")
+            if size == planned:
+                assert "tile_id=14 " in g.describe() and "split_k=1 " not in g.describe()
+            ws = torch.full((max(1, g.ws_bytes),), 0xA5, dtype=torch.uint8, device="cuda")
+            g.execute_residual(A, W, None, R, D, workspace=ws, m=rows)
+        assert untouched(D) and (D[rows:] == 0).all()
+        return D[:rows]
+
+    full = call(planned, planned)
+    for rows in (33, 64, 65):
+        assert torch.equal(call(planned, rows), full[:rows]), rows
+    for rows in (1, 32):
+        got = call(planned, rows)
+        assert torch.equal(got, call(rows, rows)), rows
+        if d == "f32":   # (another order of adding)
+            assert not torch.equal(got, full[:rows])
+        want = A[:rows].double() @ W.double().t() + R[:rows].double()
+        size = A[:rows].double().abs() @ W.double().abs().t() + R[:rows].double().abs()
+        f = torch.finfo(DT[d])
+        assert ((got.double() - want).abs() <= (k + 8) * U * size + want.abs() * f.eps / 2 * (1 + 2.0 ** -6)).all()
