@@ -179,8 +179,12 @@ int cheapest_tile(const TileCost* t, int n, const ge_desc& d) {
     return best;
 }
 
-// The residual product's tile.  E4M3 256 x 256 has its say where it gives every
-// CU two tiles (8192 x 4096 x 16384: 437 us, as 256 x 128).  Block-scaled 128 x 128:
+// The residual product's tile.  E4M3: 256 x 256 where it gives every CU two tiles,
+// else by cost.  Measured at K = 512 / 4096 / 16384, us, 256 x 256 against 256 x 128:
+// 8192 x 4096 (512 tiles of 256 x 256) 46, 130, 428 / 54, 152, 449; 8192 x 5120 (640)
+// 63, 186 / 63, 183; 8192 x 8192 (1024) 109, 286 / 116, 309; 16384 x 8192 (2048) 208,
+// 544 / 220, 612; below, 6144 x 4096 (384) 45, 116, 372 / 43, 109, 337.  (One full round,
+// 4096 x 4096, would win too: 25, 67, 214 / 32, 78, 228.)  Block-scaled 128 x 128:
 // two workgroups per CU against one with four stages and split-K: 8192 x 8192 x
 // 8192 758 / 875, 1300 x 4096 x 4096 (352 tiles) 53 / 60, 1024 x 4096 x 4096 (256) 38 / 34.
 int choose_res_tile(const ge_desc& d) {
@@ -1019,9 +1023,22 @@ static ge_desc pair_desc_b(const ge_plan_s* h) {
 
 // The tile that runs both gradients' products in one launch, or 0: not for
 // fp32, nor where a product is small enough for its plan to split its
-// reduction, nor where each fills the chip many times over.  One launch / two
-// (us): 1000 x 520 x 1032 18 / 27, 4096 x 4096 x 4096 (512 tiles of 256 x 256) 249 /
-// 407, 8192 x 4096 x 16384 (3072) 1755 / 1735.
+// reduction, nor where each fills the chip many times over.  By both products'
+// tiles together: 256 x 256 if they fill the chip, else 128 x 128 if those do, else
+// 64 x 64.  Measured, bf16, weight n x k, us (m x n x k: tiles of 256 x 256 and 128 x 128;
+// two launches, one of 256 x 256, 128 x 128, 64 x 64):
+//   512 x 512 x 512 (8, 32)         19, 21, 13, 9
+//   1000 x 520 x 1032 (35, 117)     27, 33, 20, 16
+//   2133 x 952 x 1128 (65, 225)     52, 57, 41, 35
+//   2048 x 2048 x 1024 (64, 256)    50, 49, 30, 38
+//   2048 x 2048 x 2048 (128, 512)   82, 52, 50, 61
+//   5687 x 1840 x 1232 (155, 600)   144, 129, 101, 135
+//   2048 x 1024 x 4096 (192, 768)   78, 52, 54, 61
+//   4096 x 4096 x 2048 (256, 1024)  184, 129, 153, 207
+//   4096 x 4096 x 4096 (512, 2048)  327, 228, 290, 391
+//   4096 x 16384 x 4096 (1280)      1230, 887, 1332, 1832
+//   8192 x 8192 x 8192 (2048)       1667, 1666, 2590, 4159
+//   8192 x 4096 x 16384 (3072)      1727, 1754, 2634, 3447
 static int choose_pair_tile(const ge_plan_s* h) {
     for (const ge_plan_s* g : {h->g_a, h->g_b}) {
         if (elem_size(g->d.a_type) != 2 || g->path != PATH_TILE) return 0;

@@ -6,7 +6,8 @@
 // D (rows of W) and all of K; its eight waves split K in spans of 128 bytes of
 // a row and their sums meet in LDS in wave order, so no partial sum leaves
 // the CU and the call is one launch without a workspace: an exchange between
-// workgroups costs about 6 us, as long as 30 MB of W take to stream.
+// workgroups costs 4 us and the partials' traffic (res_split in api.cpp), as
+// long as 20 MB of W take to stream and more.
 //  * A load instruction takes whole 128-byte lines (lane l: row l / 8, chunk
 //    l % 8): fetched in the operand layout (lane: row l % 16, chunk l / 16) an
 //    instruction touches 16 half lines, and the 16 x 4096 x 16384 bf16 product
