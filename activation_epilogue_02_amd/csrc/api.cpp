@@ -836,17 +836,6 @@ int gemm_epilog_execute_static(ge_handle h, const void* A, const void* B, const 
 // weights the tiles win (x, read by every workgroup, is then more bytes than W).
 static bool few_rows(const ge_desc& d, int64_t m) { return m <= 64 && d.op_b == GE_OP_T && d.a_type != GE_F32; }
 
-// Whether a call of m rows streams.  Its own rows decide, not the plan's: a handle
-// for prompts serves single tokens too, and its tiles would walk all of K in a
-// few workgroups (1 x 4096 x 16384 bf16 on a handle of 8192 rows: 258 us, 30
-// streamed).  Only where the plan has the 64 x 64 split-K tiles and they are the
-// faster ones (above: 33 rows and more, from 16 MiB of weight on) they stay.
-static bool streams(const ge_plan_s* h, int64_t m) {
-    const ge_desc& d = h->d;
-    if (!few_rows(d, m)) return false;
-    return h->path == PATH_SKINNY || h->tile_id != 14 || m <= 32 || d.n * d.k * elem_size(d.a_type) < (int64_t)16 << 20;
-}
-
 // The streaming kernel for m rows: groups of 16 rows and of 16 columns per workgroup.
 struct FewRowsShape {
     int32_t mb, rg, blocks;
@@ -989,7 +978,10 @@ int gemm_epilog_execute_residual(ge_handle h, int64_t m, const void* A, const vo
     r.row_scale = row_scale;
     r.col_scale = col_scale;
     r.ldr = ldr;
-    if (streams(h, m)) {
+    // by this call's rows, not the plan's: a handle for prompts serves single tokens too, and its
+    // tiles would walk all of K in a few workgroups (1 x 4096 x 16384 bf16 on a handle of 8192
+    // rows 258 us, streamed 30; 64 rows on handles of 100 and 300 rows 51 and 80, streamed 49)
+    if (few_rows(d, m)) {
         const FewRowsShape f = few_rows_shape(d, m);
         a.tiles_m = 1;
         a.tiles_n = f.blocks;

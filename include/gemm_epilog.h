@@ -444,8 +444,7 @@ int gemm_epilog_execute_mx(ge_handle h, const void* A, const void* B, const void
  * gemm_epilog_execute_residual launches it for m rows, 0 <= m <= the planned.
  * Up to 64 rows of a weight n x k (not fp32) take the kernel for few rows,
  * whatever the plan describes: their bits are those of a handle planned for
- * them (but 33 to 64 rows of a 16-bit weight of 16 MiB or more stay with a
- * plan's split-K tiles).  The plan's workspace suffices for every m.
+ * them.  The plan's workspace suffices for every m.
  *   a_scales, b_scales   block scales of GE_MXF8_E4M3 operands (see
  *                        execute_mx), NULL for every other type
  *   residual, ldr        R, m x n in D's type with row stride ldr elements;
