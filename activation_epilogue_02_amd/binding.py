@@ -159,60 +159,21 @@ def _stream(stream) -> Optional[int]:
 
 
 # ---- checks of the tensors a call is given -------------------------------------------
-# The kernels see addresses, sizes and row strides only, so a tensor that does not hold what the plan says would be
-# read or written out of place.  Each helper returns the address.  (Host time of a small call: an attribute of a
-# tensor takes about 0.1 us, so each is read once, and absent tensors cost no call.)
-def _matrix(t, rows, cols, ld, dtype, device, what) -> int:
-    """A matrix of at least rows x cols values with row stride ld (8-bit codes may come as bytes)."""
-    if t.dtype is not dtype and not (t.dtype is torch.uint8 and dtype is torch.float8_e4m3fn):
-        raise GemmEpilogError(GE_ERR_DTYPE, what)
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        fits = (stride == (ld, 1) or (rows == 1 or stride[0] == ld) and (cols == 1 or stride[1] == 1)) and (
-            shape[0] >= rows and shape[1] >= cols)
-    else:
-        fits = _holds_rows(t, rows, cols, ld)
-    if not fits and rows > 0 and cols > 0:
-        raise GemmEpilogError(GE_ERR_SHAPE, what)
-    if t.get_device() != device:
-        raise GemmEpilogError(GE_ERR_HIP, what + " is on another device")
-    return t.data_ptr()
+# tensor_args.cpp: each check returns the tensor's address, or raises GemmEpilogError.
+ARGS_PATH = os.path.join(_HERE, "_tensor_args.so")
+_args = None
 
 
-def _holds_rows(t, rows, cols, ld) -> bool:
-    """The same for a tensor of another rank: rows along the first dimension, or packed storage."""
-    if t.dim() > 1 and t.shape[0] >= rows and (rows == 1 or t.stride(0) == ld):
-        row = t[:1]
-        return row.is_contiguous() and row.numel() >= cols
-    return (t.is_contiguous() and (rows == 1 or t.dim() < 2 or ld in t.stride())
-            and t.numel() >= (rows - 1) * ld + cols)
-
-
-def _vector(t, count, dtype, device, what) -> int:
-    """At least `count` packed values."""
-    if t.dtype is not dtype:
-        raise GemmEpilogError(GE_ERR_DTYPE, what)
-    if t.numel() < count or not t.is_contiguous():
-        raise GemmEpilogError(GE_ERR_SHAPE, what)
-    if t.get_device() != device:
-        raise GemmEpilogError(GE_ERR_HIP, what + " is on another device")
-    return t.data_ptr()
-
-
-def _scale_rows(t, rows, ld, device, what) -> int:
-    """Block scales: rows of ld bytes, packed."""
-    if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e8m0fnu:
-        raise GemmEpilogError(GE_ERR_DTYPE, what)
-    return _vector(t, rows * ld, t.dtype, device, what)
-
-
-def _workspace(t, device, what):
-    """(address, bytes) of a packed tensor of any type."""
-    if not t.is_contiguous():
-        raise GemmEpilogError(GE_ERR_SHAPE, what)
-    if t.get_device() != device:
-        raise GemmEpilogError(GE_ERR_HIP, what + " is on another device")
-    return t.data_ptr(), t.numel() * t.element_size()
+def tensor_args():
+    """The module of the checks (loaded once).  Raises if it has not been built."""
+    global _args
+    if _args is None:
+        if not os.path.exists(ARGS_PATH):
+            raise ImportError(f"{ARGS_PATH} is missing: build it with __graft_entry__.build()")
+        from . import _tensor_args
+        _tensor_args.set_error(GemmEpilogError)
+        _args = _tensor_args
+    return _args
 
 
 def _device(t, what) -> int:
@@ -427,7 +388,7 @@ class GemmEpilog:
     def __init__(self, m, n, k, a_dtype, d_dtype, op_b=GE_OP_N, lda=None, ldb=None, ldd=None, batch=0):
         d = self.desc = make_desc(m, n, k, a_dtype, d_dtype, op_b, lda, ldb, ldd, batch=batch)
         self.h = gemm_epilog_create(self.desc)
-        self._lib = lib()
+        self._lib, self._args = lib(), tensor_args()
         # (a structure's field takes 0.1 us to read)
         self._sizes = (d.m, d.n, d.k, d.lda, d.ldd)
         self._types = (TORCH_DTYPE[d.a_type], TORCH_DTYPE[d.d_type])
@@ -482,10 +443,12 @@ class GemmEpilog:
     def _aux(self, aux, rows, device, what) -> int:
         """aux of `rows` rows as the epilogue lays it out: mask words, or the pre-activation in D's type."""
         if self.epilog == GE_EPILOG_RELU_AUX_BIAS:
-            return _matrix(aux, rows, self.aux_ld_bits // 32, self.aux_ld_bits // 32, torch.int32, device, what)
+            ld = self.aux_ld_bits // 32
+            return self._args.matrix(aux, rows, ld, ld, torch.int32, device, what)
         if self.epilog == GE_EPILOG_GELU_AUX_BIAS:
             d = self._types[1]
-            return _matrix(aux, rows, self._sizes[1], self.aux_ld_bits // torch.finfo(d).bits, d, device, what)
+            ld = self.aux_ld_bits // torch.finfo(d).bits
+            return self._args.matrix(aux, rows, self._sizes[1], ld, d, device, what)
         return aux.data_ptr()   # (this epilogue has none: refused)
 
     def execute_residual(self, A, B, bias=None, residual=None, D=None, aux=None, row_scale=None, col_scale=None,
@@ -504,34 +467,35 @@ class GemmEpilog:
         if m is not None:
             rows = m
         a_type, d_type = self._types
+        matrix, vector, scale_rows = self._args.matrix, self._args.vector, self._args.scale_rows
         dev = _device(D, "execute_residual: D")
-        d = _matrix(D, rows, n, ldr, d_type, dev, "execute_residual: D")
-        a = None if A is None else _matrix(A, rows, k, lda, a_type, dev, "execute_residual: A")
-        b = None if B is None else _matrix(B, *self._weight, a_type, dev, "execute_residual: B")
+        d = matrix(D, rows, n, ldr, d_type, dev, "execute_residual: D")
+        a = None if A is None else matrix(A, rows, k, lda, a_type, dev, "execute_residual: A")
+        b = None if B is None else matrix(B, *self._weight, a_type, dev, "execute_residual: B")
         r = bv = rs = cs = sa = sb = fa = fb = ax = ws = None
         ws_bytes, f32 = 0, torch.float32
         if residual is not None:
             if rows > 1:   # (a single row has no stride of its own)
                 ldr = residual.stride(0)
-            r = _matrix(residual, rows, n, ldr, d_type, dev, "execute_residual: residual")
+            r = matrix(residual, rows, n, ldr, d_type, dev, "execute_residual: residual")
         if bias is not None:
-            bv = _vector(bias, rows if self.axis == GE_BIAS_ROW else n, d_type, dev, "execute_residual: bias")
+            bv = vector(bias, rows if self.axis == GE_BIAS_ROW else n, d_type, dev, "execute_residual: bias")
         if row_scale is not None:
-            rs = _vector(row_scale, rows, f32, dev, "execute_residual: row_scale")
+            rs = vector(row_scale, rows, f32, dev, "execute_residual: row_scale")
         if col_scale is not None:
-            cs = _vector(col_scale, n, f32, dev, "execute_residual: col_scale")
+            cs = vector(col_scale, n, f32, dev, "execute_residual: col_scale")
         if a_scales is not None:
-            sa = _scale_rows(a_scales, rows, mx_scale_ld(k), dev, "execute_residual: a_scales")
+            sa = scale_rows(a_scales, rows, mx_scale_ld(k), dev, "execute_residual: a_scales")
         if b_scales is not None:
-            sb = _scale_rows(b_scales, n, mx_scale_ld(k), dev, "execute_residual: b_scales")
+            sb = scale_rows(b_scales, n, mx_scale_ld(k), dev, "execute_residual: b_scales")
         if scale_a is not None:
-            fa = _vector(scale_a, 1, f32, dev, "execute_residual: scale_a")
+            fa = vector(scale_a, 1, f32, dev, "execute_residual: scale_a")
         if scale_b is not None:
-            fb = _vector(scale_b, 1, f32, dev, "execute_residual: scale_b")
+            fb = vector(scale_b, 1, f32, dev, "execute_residual: scale_b")
         if aux is not None:
             ax = self._aux(aux, rows, dev, "execute_residual: aux")
         if workspace is not None:
-            ws, ws_bytes = _workspace(workspace, dev, "execute_residual: workspace")
+            ws, ws_bytes = self._args.workspace(workspace, dev, "execute_residual: workspace")
         _check(self._lib.gemm_epilog_execute_residual(self.h, rows, a, b, sa, sb, bv, r, ldr, rs, cs, fa, fb, d, ax, ws,
                                                       ws_bytes, _stream(stream)), "gemm_epilog_execute_residual")
         return D, aux
@@ -547,19 +511,21 @@ class GemmEpilog:
 
         Every tensor is checked against the plan as in execute_residual."""
         m, n, k, lda, ldd = self._sizes
-        t = self._types[0]
+        t, matrix = self._types[0], self._args.matrix
         first = next((v for v in (dD, A, B, dA, dB, dbias) if v is not None), None)
         dev = -1 if first is None else _device(first, "backward: dD")
-        dd = None if dD is None else _matrix(dD, m, n, ldd, t, dev, "backward: dD")
+        dd = None if dD is None else matrix(dD, m, n, ldd, t, dev, "backward: dD")
         # (the library refuses the absence of what a wanted gradient reads)
-        a = None if A is None else _matrix(A, m, k, lda, t, dev, "backward: A")
-        b = None if B is None else _matrix(B, *self._weight, t, dev, "backward: B")
-        ga = None if dA is None else _matrix(dA, m, k, lda, t, dev, "backward: dA")
-        gb = None if dB is None else _matrix(dB, *self._weight, t, dev, "backward: dB")
+        a = None if A is None else matrix(A, m, k, lda, t, dev, "backward: A")
+        b = None if B is None else matrix(B, *self._weight, t, dev, "backward: B")
+        ga = None if dA is None else matrix(dA, m, k, lda, t, dev, "backward: dA")
+        gb = None if dB is None else matrix(dB, *self._weight, t, dev, "backward: dB")
         gv = (None if dbias is None
-              else _vector(dbias, m if self.axis == GE_BIAS_ROW else n, t, dev, "backward: dbias"))
+              else self._args.vector(dbias, m if self.axis == GE_BIAS_ROW else n, t, dev, "backward: dbias"))
         ax = None if aux is None else self._aux(aux, m, dev, "backward: aux")
-        ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace, dev, "backward: workspace")
+        ws, ws_bytes = None, 0
+        if workspace is not None:
+            ws, ws_bytes = self._args.workspace(workspace, dev, "backward: workspace")
         _check(self._lib.gemm_epilog_backward(self.h, dd, a, b, ax, ga, gb, gv, ws, ws_bytes, _stream(stream)),
                "gemm_epilog_backward")
         return dA, dB, dbias

@@ -1,4 +1,5 @@
-"""Build the gfx950 shared library libgemm_epilog.so in-tree with hipcc.
+"""Build the gfx950 shared library libgemm_epilog.so in-tree with hipcc, and
+the Python module _tensor_args.so (host code) with g++.
 
 Each translation unit is compiled to an object in parallel, then linked.
 The library links the HIP runtime by name; loaded after ``import torch`` it
@@ -12,10 +13,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgemm_epilog.so")
+ARGS = os.path.join(HERE, "_tensor_args.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -49,9 +52,28 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_tensor_args() -> str:
+    """The Python module of the tensor checks (host code against torch's C++ interface)."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    tmp = ARGS + ".tmp%d" % os.getpid()
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(HERE, "tensor_args.cpp"),
+            "-I" + sysconfig.get_paths()["include"]] + ["-isystem" + p for p in include_paths()]
+           + ["-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for tensor_args.cpp:\n{r.stderr}")
+    os.replace(tmp, ARGS)
+    return ARGS
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source for gfx950 and link libgemm_epilog.so."""
+    """Compile every source for gfx950 and link libgemm_epilog.so; compile _tensor_args.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    args = build_tensor_args()
     jobs = min(len(SOURCES), max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
         objs = list(ex.map(_compile, SOURCES))
@@ -62,14 +84,15 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print("built", LIB)
+        print("built", LIB, args)
     return LIB
 
 
 def clean() -> None:
     shutil.rmtree(BUILD_DIR, ignore_errors=True)
-    if os.path.exists(LIB):
-        os.remove(LIB)
+    for f in (LIB, ARGS):
+        if os.path.exists(f):
+            os.remove(f)
 
 
 if __name__ == "__main__":

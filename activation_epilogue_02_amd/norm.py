@@ -7,8 +7,8 @@ import ctypes
 
 import torch
 
-from .binding import (DTYPE_CODE, ELEM_SIZE, TORCH_DTYPE, _check, _device, _matrix, _scale_rows, _stream, _vector,
-                      _workspace, ge_norm_desc, lib, mx_scale_ld)
+from .binding import (DTYPE_CODE, ELEM_SIZE, TORCH_DTYPE, _check, _device, _stream, ge_norm_desc, lib, mx_scale_ld,
+                      tensor_args)
 
 GE_NORM_PLAIN, GE_NORM_E4M3_ROW, GE_NORM_MX = 0, 1, 2
 NORM_OUT_CODE = {"plain": GE_NORM_PLAIN, "e4m3_row": GE_NORM_E4M3_ROW, "mx": GE_NORM_MX}
@@ -36,7 +36,7 @@ class RmsNorm:
         self.desc = ge_norm_desc(rows, cols, t, o, -(-cols // e) * e if ld is None else ld,
                                  -(-cols // ey) * ey if ldy is None else ldy, eps)
         h = ctypes.c_void_p()
-        self._lib = lib()
+        self._lib, self._args = lib(), tensor_args()
         _check(self._lib.ge_rms_norm_create(ctypes.byref(h), ctypes.byref(self.desc)), "ge_rms_norm_create")
         self.h = h.value
         self.rows, self.cols, self.ld, self.ldy = rows, cols, self.desc.ld, self.desc.ldy
@@ -62,19 +62,20 @@ class RmsNorm:
         Every tensor has to hold those rows in the handle's types and strides: GemmEpilogError with GE_ERR_DTYPE or
         GE_ERR_SHAPE otherwise (GE_ERR_HIP: not on the current GPU, whose stream takes the launch)."""
         n, cols, ld, t = self.rows if rows is None else rows, self.cols, self.ld, self.dtype
+        matrix, vector = self._args.matrix, self._args.vector
         first = y if y is not None else gamma   # (the library refuses what is missing)
         dev = -1 if first is None else _device(first, "RmsNorm.forward: y")
-        xp = None if x is None else _matrix(x, n, cols, ld, t, dev, "RmsNorm.forward: x")
-        rp = None if residual is None else _matrix(residual, n, cols, ld, t, dev, "RmsNorm.forward: residual")
-        gp = None if gamma is None else _vector(gamma, cols, t, dev, "RmsNorm.forward: gamma")
-        hp = None if h is None else _matrix(h, n, cols, ld, t, dev, "RmsNorm.forward: h")
-        yp = None if y is None else _matrix(y, n, cols, self.ldy, self.out_dtype, dev, "RmsNorm.forward: y")
+        xp = None if x is None else matrix(x, n, cols, ld, t, dev, "RmsNorm.forward: x")
+        rp = None if residual is None else matrix(residual, n, cols, ld, t, dev, "RmsNorm.forward: residual")
+        gp = None if gamma is None else vector(gamma, cols, t, dev, "RmsNorm.forward: gamma")
+        hp = None if h is None else matrix(h, n, cols, ld, t, dev, "RmsNorm.forward: h")
+        yp = None if y is None else matrix(y, n, cols, self.ldy, self.out_dtype, dev, "RmsNorm.forward: y")
         sp = None
         if scales is not None:
-            sp = (_scale_rows(scales, n, self.scale_ld, dev, "RmsNorm.forward: scales")
+            sp = (self._args.scale_rows(scales, n, self.scale_ld, dev, "RmsNorm.forward: scales")
                   if self.scale_dtype is torch.uint8 else
-                  _vector(scales, n, torch.float32, dev, "RmsNorm.forward: scales"))
-        vp = None if rstd is None else _vector(rstd, n, torch.float32, dev, "RmsNorm.forward: rstd")
+                  vector(scales, n, torch.float32, dev, "RmsNorm.forward: scales"))
+        vp = None if rstd is None else vector(rstd, n, torch.float32, dev, "RmsNorm.forward: rstd")
         _check(self._lib.ge_rms_norm_forward(self.h, n, xp, rp, gp, hp, yp, sp, vp, _stream(stream)),
                "ge_rms_norm_forward")
 
@@ -82,16 +83,19 @@ class RmsNorm:
         """Writes dx (the gradient of x and of the residual) and, if given,
         dgamma, which needs a workspace of workspace_bytes.  Checks as forward's."""
         n, cols, ld, t = self.rows if rows is None else rows, self.cols, self.ld, self.dtype
+        matrix, vector = self._args.matrix, self._args.vector
         first = dx if dx is not None else gamma
         dev = -1 if first is None else _device(first, "RmsNorm.backward: dx")
-        yp = None if dy is None else _matrix(dy, n, cols, ld, t, dev, "RmsNorm.backward: dy")
-        hp = None if h is None else _matrix(h, n, cols, ld, t, dev, "RmsNorm.backward: h")
-        gp = None if gamma is None else _vector(gamma, cols, t, dev, "RmsNorm.backward: gamma")
-        vp = None if rstd is None else _vector(rstd, n, torch.float32, dev, "RmsNorm.backward: rstd")
-        ep = None if dh is None else _matrix(dh, n, cols, ld, t, dev, "RmsNorm.backward: dh")
-        xp = None if dx is None else _matrix(dx, n, cols, ld, t, dev, "RmsNorm.backward: dx")
-        dp = None if dgamma is None else _vector(dgamma, cols, t, dev, "RmsNorm.backward: dgamma")
-        ws, size = (None, 0) if workspace is None else _workspace(workspace, dev, "RmsNorm.backward: workspace")
+        yp = None if dy is None else matrix(dy, n, cols, ld, t, dev, "RmsNorm.backward: dy")
+        hp = None if h is None else matrix(h, n, cols, ld, t, dev, "RmsNorm.backward: h")
+        gp = None if gamma is None else vector(gamma, cols, t, dev, "RmsNorm.backward: gamma")
+        vp = None if rstd is None else vector(rstd, n, torch.float32, dev, "RmsNorm.backward: rstd")
+        ep = None if dh is None else matrix(dh, n, cols, ld, t, dev, "RmsNorm.backward: dh")
+        xp = None if dx is None else matrix(dx, n, cols, ld, t, dev, "RmsNorm.backward: dx")
+        dp = None if dgamma is None else vector(dgamma, cols, t, dev, "RmsNorm.backward: dgamma")
+        ws, size = None, 0
+        if workspace is not None:
+            ws, size = self._args.workspace(workspace, dev, "RmsNorm.backward: workspace")
         _check(self._lib.ge_rms_norm_backward(self.h, n, yp, hp, gp, vp, ep, xp, dp, ws, size, _stream(stream)),
                "ge_rms_norm_backward")
 

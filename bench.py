@@ -487,7 +487,7 @@ def main():
     import synth
     from activation_epilogue_02_amd import binding as B
 
-    if not os.path.exists(B.LIB_PATH):
+    if not (os.path.exists(B.LIB_PATH) and os.path.exists(B.ARGS_PATH)):
         import __graft_entry__
         __graft_entry__.build()
 

@@ -296,3 +296,25 @@ def test_tensors_of_another_gpu(monkeypatch):
     monkeypatch.setattr(B, "_raw_device", None)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     assert B._device(On(0), "x") == 0
+
+
+def test_arguments_of_the_checks():
+    """What is no tensor, type or number is a TypeError, as is a wrong count; a value beyond 64 bits an OverflowError."""
+    m = B.tensor_args()
+    t, f = torch.zeros(4, 8), torch.float32
+    assert m.matrix(t, 4, 8, 8, f, -1, "t") == t.data_ptr() and m.vector(t, 32, f, -1, "t") == t.data_ptr()
+    assert m.workspace(t, -1, "t") == (t.data_ptr(), 128)
+    assert m.matrix(t[:0], 0, 8, 8, f, -1, "t") == t[:0].data_ptr()
+    for call in (lambda: m.matrix(1, 4, 8, 8, f, -1, "t"), lambda: m.matrix(t, "4", 8, 8, f, -1, "t"),
+                 lambda: m.matrix(t, 4, 8, 8, "f32", -1, "t"), lambda: m.matrix(t, 4, 8, 8, f, -1, None),
+                 lambda: m.matrix(t, 4, 8), lambda: m.vector(None, 4, f, -1, "t"), lambda: m.vector(t, 4, f),
+                 lambda: m.scale_rows(t, None, 4, -1, "t"), lambda: m.workspace(t, None, "t"),
+                 lambda: m.workspace([], -1, "t")):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(OverflowError):
+        m.matrix(t, 1 << 70, 8, 8, f, -1, "t")
+    with pytest.raises(B.GemmEpilogError, match="t is on another device"):
+        m.matrix(t, 4, 8, 8, f, 0, "t")
+    with pytest.raises(RuntimeError):                                 # (a tensor without storage)
+        m.vector(torch.zeros(4).to_sparse(), 4, f, -1, "t")
