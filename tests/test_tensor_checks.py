@@ -278,7 +278,8 @@ def test_stream_without_internal_calls(monkeypatch):
     spec = importlib.util.spec_from_file_location("binding_again", B.__file__)
     fresh = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fresh)
-    assert fresh._stream(None) is None and fresh._stream(7) == 7      # (no GPU in use)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: False)
+    assert fresh._stream(None) is None and fresh._stream(7) == 7
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=0x1234))
     assert fresh._stream(None) == 0x1234
